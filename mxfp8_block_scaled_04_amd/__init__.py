@@ -457,3 +457,9 @@ def mx_grouped_gemm_wgrad(A, As, B, Bs, padded_offsets, dW=None, stream=None):
                                       _ptr(dW), _stream(stream))
     _check(rc, "mx_grouped_gemm_wgrad")
     return dW
+
+
+# The training step of unquantized experts (include/libmxmoe_train.h).
+from .training import (  # noqa: E402
+    TRAIN_SYMBOLS, AdamWPlan, mx_adamw, mx_adamw_plan, mx_grad_norm, mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad,
+    mx_grouped_gemm_bf16_wgrad)

@@ -1,0 +1,365 @@
+// The optimizer step over many tensors at once: AdamW with states in 32 or
+// in 8 bits, and the global norm of the gradients that clips it.
+//
+// Mathematics (fp32, per element; t = step count after this step, c = the
+// gradients' factor):
+//   g' = c g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+//   w  = (1 - lr d) w - [lr / (1 - b1^t)] m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+// 8-bit states hold m and sqrt(v) as E4M3 codes under one fp32 scale per 256
+// elements, scale = max(amax, 2^-100) / 448.  sqrt(v) and not v: E4M3 spans
+// 2^17.8 from its smallest code to 448, which is 2^35 in v.  The scale is a
+// float and not a power of two so that it follows the block's largest value
+// as that decays by less than a code's step; the other codes of the block
+// keep their ratio to it.  Codes of v > 0 are never zero: m / eps would
+// follow in a later step.
+//
+// What bounds it: HBM.  Nothing is read twice; per element 12 to 30 bytes
+// move and about 50 vector operations run (the vector units could run about
+// 180 in the time of 28 bytes).
+//
+// Layout: one launch for all tensors.  The plan cuts every tensor into
+// chunks of 4096 elements and names the tensor of each; workgroups of 4
+// waves take chunks with a stride of the grid.  A wave takes 256 consecutive
+// elements at a time, 4 per lane, so that every load and store of a wave is
+// one contiguous piece (256 B of codes to 1 KB of floats) and a block of an
+// 8-bit state is exactly one wave: its maximum is a reduction in registers.
+#include <type_traits>
+
+#include "mx_train.h"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 4;                                 // elements per lane and block
+constexpr int kBlocks = kAdamwChunk / (64 * kPer) / 4;  // blocks of 256 per wave and chunk
+static_assert(64 * kPer == MX_ADAMW_BLOCK, "a wave is a block");
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Constants of a step, the same in every lane.
+struct Step {
+    float c;          // factor of the gradients
+    float b1, a1;     // beta1, 1 - beta1
+    float b2, a2;     // beta2, 1 - beta2
+    float lr;
+    float size;       // lr / (1 - beta1^t)
+    float root;       // 1 / sqrt(1 - beta2^t)
+    float eps;
+};
+
+__device__ __forceinline__ double power(double b, int64_t t) {
+    double r = 1.0;
+    for (uint64_t e = (uint64_t)t; e != 0; e >>= 1, b *= b)
+        if (e & 1) r *= b;
+    return r;
+}
+
+// Largest value over the wave's 64 lanes (non-negative values).
+__device__ __forceinline__ float wave_max(float v) {
+    const auto dpp = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                                  0xF, 0xF, false));
+    };
+    v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>{}));   // quad_perm [1,0,3,2]
+    v = fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>{}));   // quad_perm [2,3,0,1]
+    v = fmaxf(v, dpp(v, std::integral_constant<int, 0x141>{}));  // row_half_mirror
+    v = fmaxf(v, dpp(v, std::integral_constant<int, 0x140>{}));  // row_mirror
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]), __builtin_bit_cast(float, (uint32_t)q[1]));
+}
+
+// 4 consecutive elements from i on, as float.  `live`: how many of them exist
+// (0 to 4); the others read as zero.  With `fast` all 4 exist and are aligned.
+__device__ __forceinline__ void load4(const float* p, int64_t i, int live, bool fast, float (&v)[4]) {
+    if (fast) {
+        const f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
+        for (int e = 0; e < 4; ++e) v[e] = x[e];
+    } else {
+        for (int e = 0; e < 4; ++e) v[e] = e < live ? p[i + e] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, int64_t i, int live, bool fast, float (&v)[4]) {
+    if (fast) {
+        const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + i));
+        v[0] = __builtin_bit_cast(float, x[0] << 16);
+        v[1] = __builtin_bit_cast(float, x[0] & 0xFFFF0000u);
+        v[2] = __builtin_bit_cast(float, x[1] << 16);
+        v[3] = __builtin_bit_cast(float, x[1] & 0xFFFF0000u);
+    } else {
+        for (int e = 0; e < 4; ++e) v[e] = e < live ? __builtin_bit_cast(float, (uint32_t)p[i + e] << 16) : 0.0f;
+    }
+}
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int live, bool fast) {
+    if (fast) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + i));
+    uint32_t x = 0;
+    for (int e = 0; e < 4; ++e) x |= (e < live ? (uint32_t)p[i + e] : 0u) << (8 * e);
+    return x;
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int live, bool fast, const float (&v)[4]) {
+    if (fast) {
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p + i));
+    } else {
+        for (int e = 0; e < 4; ++e)
+            if (e < live) p[i + e] = v[e];
+    }
+}
+// rounded to nearest even (the weights' only rounding to fewer bits)
+__device__ __forceinline__ void store4(uint16_t* p, int64_t i, int live, bool fast, const float (&v)[4]) {
+    uint16_t b[4];
+    for (int e = 0; e < 4; ++e) b[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
+    if (fast) {
+        const u32x2 x{(uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16)};
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x2*>(p + i));
+    } else {
+        for (int e = 0; e < 4; ++e)
+            if (e < live) p[i + e] = b[e];
+    }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int live, bool fast, uint32_t x) {
+    if (fast) {
+        __builtin_nontemporal_store(x, reinterpret_cast<uint32_t*>(p + i));
+    } else {
+        for (int e = 0; e < 4; ++e)
+            if (e < live) p[i + e] = (uint8_t)(x >> (8 * e));
+    }
+}
+
+__device__ __forceinline__ void decode4(uint32_t x, float (&v)[4]) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x, false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x, true);
+    v[0] = lo[0];
+    v[1] = lo[1];
+    v[2] = hi[0];
+    v[3] = hi[1];
+}
+__device__ __forceinline__ uint32_t encode4(const float (&v)[4]) {
+    int x = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    x = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], x, true);
+    return (uint32_t)x;
+}
+
+constexpr float kTiny = 0x1p-100f;  // smallest block maximum that a scale is made for
+constexpr float kTop = 448.0f;      // largest E4M3 value
+constexpr float kLeast = 0x1p-9f;   // smallest E4M3 value
+
+// Value scaled for a code: not past the largest one (x / amax may round
+// up); a NaN passes.
+__device__ __forceinline__ float in_range(float y) { return y > kTop ? kTop : (y < -kTop ? -kTop : y); }
+
+// One chunk of one tensor.  W: 0 float32 weights, 1 bf16 weights with
+// float32 masters, 2 bf16 weights alone.
+template <int W, bool GB, bool S8>
+__device__ __forceinline__ void step_chunk(const mx_adamw_tensor& t, int64_t chunk, const Step& s, int wave, int lane) {
+    typedef typename std::conditional<GB, uint16_t, float>::type grad_t;
+    const grad_t* const gp = (const grad_t*)t.g;
+    const bool vec = (t.types & kAdamwAligned) != 0;
+    const float keep = 1.0f - s.lr * t.weight_decay;
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t block = chunk * (kAdamwChunk / MX_ADAMW_BLOCK) + u * 4 + wave;
+        const int64_t first = block * MX_ADAMW_BLOCK;
+        if (first >= t.n) break;  // the same in every lane of the wave
+        const int64_t i = first + lane * kPer;
+        const int64_t left = t.n - i;
+        const int live = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
+        const bool fast = vec && live == 4;
+        float g[4], m[4], v[4], w[4];
+        load4(gp, i, live, fast, g);
+        float ms = 0.0f, vs = 0.0f;
+        if (S8) {
+            ms = t.m_scale[block];
+            vs = t.v_scale[block];
+            decode4(load_codes((const uint8_t*)t.m, i, live, fast), m);
+            decode4(load_codes((const uint8_t*)t.v, i, live, fast), v);
+        } else {
+            load4((const float*)t.m, i, live, fast, m);
+            load4((const float*)t.v, i, live, fast, v);
+        }
+        if (W == 0) load4((const float*)t.w, i, live, fast, w);
+        if (W == 1) load4(t.master, i, live, fast, w);
+        if (W == 2) load4((const uint16_t*)t.w, i, live, fast, w);
+        float r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (S8) {
+                m[e] *= ms;
+                v[e] *= vs;
+                v[e] *= v[e];
+            }
+            const float x = g[e] * s.c;
+            m[e] = fmaf(s.b1, m[e], s.a1 * x);
+            v[e] = fmaf(s.b2, v[e], s.a2 * x * x);
+            r[e] = __builtin_sqrtf(v[e]);
+            const float update = m[e] / fmaf(r[e], s.root, s.eps);
+            w[e] = fmaf(-s.size, update, keep * w[e]);
+        }
+        if (W == 0) store4((float*)t.w, i, live, fast, w);
+        if (W == 1) store4(t.master, i, live, fast, w);
+        if (W != 0) store4((uint16_t*)t.w, i, live, fast, w);
+        if (S8) {
+            float am = 0.0f, av = 0.0f;  // (lanes past the end hold zeros)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                am = fmaxf(am, fabsf(m[e]));
+                av = fmaxf(av, r[e]);
+            }
+            am = fmaxf(wave_max(am), kTiny);
+            av = fmaxf(wave_max(av), kTiny);
+            const float im = kTop / am, iv = kTop / av;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                m[e] = in_range(m[e] * im);
+                const float y = in_range(r[e] * iv);
+                v[e] = r[e] > 0.0f && y < kLeast ? kLeast : y;
+            }
+            store_codes((uint8_t*)t.m, i, live, fast, encode4(m));
+            store_codes((uint8_t*)t.v, i, live, fast, encode4(v));
+            if (lane == 0) {
+                t.m_scale[block] = am / kTop;
+                t.v_scale[block] = av / kTop;
+            }
+        } else {
+            store4((float*)t.m, i, live, fast, m);
+            store4((float*)t.v, i, live, fast, v);
+        }
+    }
+}
+
+template <int W, bool GB>
+__device__ __forceinline__ void step_state(const mx_adamw_tensor& t, int64_t chunk, const Step& s, int wave, int lane) {
+    if (t.types & MX_ADAMW_STATE_8BIT) step_chunk<W, GB, true>(t, chunk, s, wave, lane);
+    else step_chunk<W, GB, false>(t, chunk, s, wave, lane);
+}
+template <int W>
+__device__ __forceinline__ void step_grad(const mx_adamw_tensor& t, int64_t chunk, const Step& s, int wave, int lane) {
+    if (t.types & MX_ADAMW_G_BF16) step_state<W, true>(t, chunk, s, wave, lane);
+    else step_state<W, false>(t, chunk, s, wave, lane);
+}
+
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
+    __shared__ int64_t done;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const float c = a.grad_scale ? *a.grad_scale : 1.0f;
+    const bool skip = !(c >= 0.0f && c <= __FLT_MAX__);
+    if (threadIdx.x == 0) {
+        // the count is read before the ticket is drawn, and the last
+        // workgroup to draw one raises it: every workgroup has read it then
+        const int64_t t = __hip_atomic_load(a.steps, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        done = t;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const int64_t ticket = __hip_atomic_fetch_add(a.steps + 1, (int64_t)1, __ATOMIC_RELAXED,
+                                                      __HIP_MEMORY_SCOPE_AGENT);
+        if (ticket == (int64_t)gridDim.x - 1) {
+            __hip_atomic_store(a.steps + 1, (int64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (!skip) __hip_atomic_store(a.steps, t + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    __syncthreads();
+    if (skip) return;
+    const int64_t t = done + 1;
+    Step s;
+    s.c = c;
+    s.b1 = (float)a.beta1;
+    s.a1 = (float)(1.0 - a.beta1);
+    s.b2 = (float)a.beta2;
+    s.a2 = (float)(1.0 - a.beta2);
+    const double lr = a.lr_device ? (double)*a.lr_device : a.lr;
+    s.lr = (float)lr;
+    s.size = (float)(lr / (1.0 - power(a.beta1, t)));
+    s.root = (float)(1.0 / sqrt(1.0 - power(a.beta2, t)));
+    s.eps = (float)a.eps;
+    for (int64_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+        const AdamwEntry* const e = a.entries + a.owner[k];
+        const mx_adamw_tensor tensor = e->t;
+        const int64_t chunk = k - e->first_chunk;
+        if (!(tensor.types & MX_ADAMW_W_BF16)) step_grad<0>(tensor, chunk, s, wave, lane);
+        else if (tensor.master) step_grad<1>(tensor, chunk, s, wave, lane);
+        else step_grad<2>(tensor, chunk, s, wave, lane);
+    }
+}
+
+// Sum of squares of one chunk, in double: squares of finite gradients do not
+// overflow there, and a sum over 10^9 elements keeps far more than the 24
+// bits of the result.
+template <typename T>
+__device__ __forceinline__ void norm_chunk(const mx_adamw_tensor& t, int64_t chunk, int wave, int lane, double& sum) {
+    const bool vec = (t.types & kAdamwAligned) != 0;
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t i = chunk * kAdamwChunk + (u * 4 + wave) * MX_ADAMW_BLOCK + lane * kPer;
+        const int64_t left = t.n - i;
+        const int live = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
+        float g[4];
+        load4((const T*)t.g, i, live, vec && live == 4, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = fma((double)g[e], (double)g[e], sum);
+    }
+}
+
+// Sum over the workgroup (valid in thread 0), in a fixed order.
+__device__ __forceinline__ double group_sum(double v, double* part) {
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_down(v, d, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return part[0] + part[1] + part[2] + part[3];
+}
+
+// Each workgroup sums the chunks k = blockIdx, blockIdx + grid, ... in order;
+// the last one to finish sums the workgroups' results in order.
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const AdamwEntry* entries, const int32_t* owner,
+                                                             int64_t chunks, float max_norm, NormWorkspace* ws,
+                                                             float* out) {
+    __shared__ double part[4], part2[4];
+    __shared__ bool last;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    double sum = 0.0;
+    for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const AdamwEntry* const e = entries + owner[k];
+        if (e->t.types & MX_ADAMW_G_BF16) norm_chunk<uint16_t>(e->t, k - e->first_chunk, wave, lane, sum);
+        else norm_chunk<float>(e->t, k - e->first_chunk, wave, lane, sum);
+    }
+    const double total = group_sum(sum, part);
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(ws->part + blockIdx.x, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = __hip_atomic_fetch_add(&ws->ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    double v = 0.0;
+    for (int k = threadIdx.x; k < (int)gridDim.x; k += kThreads)
+        v += __hip_atomic_load(ws->part + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const double all = group_sum(v, part2);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(all);
+        const float rounded = (float)norm;
+        out[0] = rounded;
+        out[1] = rounded <= __FLT_MAX__ ? (norm > (double)max_norm ? (float)(max_norm / norm) : 1.0f)
+                                        : __builtin_nanf("");
+        __hip_atomic_store(&ws->ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwArgs& a, hipStream_t stream) {
+    const int64_t most = 2048;  // 8 workgroups of 4 waves on each of 256 CUs
+    const unsigned grid = (unsigned)(a.chunks < 1 ? 1 : (a.chunks < most ? a.chunks : most));
+    hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_norm(const AdamwEntry* entries, const int32_t* owner, int64_t chunks, float max_norm,
+                            NormWorkspace* ws, float* out, hipStream_t stream) {
+    const unsigned grid = (unsigned)(chunks < 1 ? 1 : (chunks < kNormParts ? chunks : kNormParts));
+    hipLaunchKernelGGL(grad_norm_kernel, dim3(grid), dim3(kThreads), 0, stream, entries, owner, chunks, max_norm, ws,
+                       out);
+    return hipGetLastError();
+}
+
+}  // namespace mx
