@@ -13,34 +13,46 @@
 // What bounds it: the matrix pipes, where groups have many rows; reading the
 // weights, where they have few.
 //
-// Layout: persistent workgroups (one 256 x 256 tile per CU with 8 waves of
-// 128 x 64, or two 128 x 128 tiles per CU with 4 waves of 64 x 64 each),
+// Layout: persistent workgroups of 4 waves, one 256 x 256 tile per CU (128 x
+// 128 per wave) or two 128 x 128 tiles per CU (64 x 64 per wave),
 // v_mfma_f32_32x32x16_bf16.  A stage is 64 contraction elements of both
 // operands (64 KB for the large tile), loaded straight into LDS by 16-byte
-// direct loads, two stages in LDS.  Within a stage there are 4 steps of 16;
-// the fragments of a step are read while the one before is multiplied, also
-// across stages and tiles: the wait for the next stage and the barrier sit
-// before a stage's last step, whose fragments are in registers by then, and
-// the loads of the stage after the next go into the buffer freed by that
-// barrier.
+// direct loads; two stages in LDS.  A stage has 4 steps of 16: the fragments
+// of a step are read while the one before is multiplied, also across stages
+// and tiles.  The wait for the next stage and the barrier sit before a
+// stage's last step, whose fragments are in registers by then; the loads of
+// the stage after the next go into the buffer freed by that barrier, spread
+// over two steps.
+// Tried and slower at 32768 x 4096 x 7168 (16 groups, 1.63 ms as it is, 1.18
+// ms without its loads): 8 waves of 128 x 64 (1.73 ms: a third more LDS
+// reads), the same in two groups of opposite phase (1.72 ms), stages of 32
+// with 4 in LDS (1.78 ms: 64-byte pieces of rows double the requests to L2),
+// all loads in one step (1.74 ms), loads spread over three (1.63 ms).
 //
 // Bounds: all loads go through buffer descriptors that end at the operand's
 // last valid element; what lies past it reads as zero.  Rows of a tile past
 // its group, contraction indices past K (N for dgrad, the group's rows for
 // wgrad) and stages past the last tile need no other care, except granules
 // past K inside a row, whose offsets are moved out of range.
+#include <type_traits>
+
 #include "mx_train.h"
 
 namespace mx {
 namespace {
 
 constexpr int SK = 64;          // contraction elements per stage
+constexpr int kSteps = SK / 16;  // matrix instructions along it
+constexpr int kRing = 2;        // stages in LDS
 constexpr int kLptGroups = 512;  // wgrad: groups taken longest first up to this many
 constexpr int kBand = 4;         // row tiles per band of the tile order
 // An offset past every descriptor (fewer than 2^31 bytes: 256 rows of fewer
 // than 2^22 elements), which no scalar offset of a load (below 2^31 too)
 // carries past 2^32.
 constexpr uint32_t kOut = 0x80000000u;
+// The same for the result, whose tile can span up to 2^32 - 8192 bytes and
+// whose accesses have no scalar offset.
+constexpr uint32_t kOutStore = 0xFFFFFFF0u;
 
 typedef __attribute__((address_space(3))) void lds_t;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -81,20 +93,29 @@ __device__ __forceinline__ i32x4 descriptor(const void* base, uint32_t bytes) {
 }
 
 // 16 bytes per lane from the descriptor straight into LDS, lane l to
-// [lds + 16 l, lds + 16 l + 16).  In assembly without an output register:
-// the compiler would otherwise wait for it before every LDS read.  It is
-// waited for by wait_loads and a barrier before the data is read.
+// [lds + OFF + 16 l, lds + OFF + 16 l + 16).  In assembly without an output
+// register: the compiler would otherwise wait for it before every LDS read.
+// It is waited for by wait_loads and a barrier before the data is read.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
+template <int OFF>
 __device__ __forceinline__ void load_to_lds(const i32x4& rs, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rs),
-                 "s"(soff), "s"(lds)
-                 : "memory", "m0");
+    asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rs),
+                 "s"(soff), "s"(lds), "n"(OFF)
+                 : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A barrier of the workgroup at which this wave's LDS reads are complete and
+// over which the compiler moves nothing.  (No wait for its loads to LDS.)
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Range-checked stores and loads of the result.
@@ -108,47 +129,117 @@ __device__ __forceinline__ rsrc_t out_rsrc(void* base, uint32_t bytes) {
 // ROWS elements of the tile x SK contraction elements, 128 ROWS bytes.
 //
 // T = false: row r at 128 r, its 16-byte granule c (contraction 8 c ...) at
-// position c ^ ((r >> 1) & 7): a fragment read (64 lanes, rows 0..31, two
-// neighbouring granules) then meets each bank as often as every other.
+// position c ^ (r >> 1 & 7).  A fragment read takes one granule of each of 32
+// rows and is served 16 lanes (256 bytes) at a time; the swizzle spreads them
+// over all banks.
 //
 // T = true: contraction row k at 2 ROWS k; its 32-byte unit u (tile rows 16 u
 // ...) at position u ^ f(k), f(k) = 2 (k & 3) | (k >> 3 & 1).  A transposing
 // read of 64 lanes takes 64 bytes from each of the 8 contraction rows
 // k0 + {0..3, 8..11}; f puts them into different banks.
-template <int ROWS, int WAVES, bool T>
-struct Operand {
-    static constexpr int kBytes = ROWS * SK * 2;
-    static constexpr int kLoads = kBytes / 1024 / WAVES;  // load instructions per wave and stage
-    // contraction rows (T) or tile rows of one load instruction
-    static constexpr int kRowsPerLoad = T ? 64 / (ROWS / 8) : 8;
 
-    __device__ __forceinline__ static uint32_t swizzled(uint32_t row, uint32_t pos) {
-        if (T) {
-            const uint32_t f = ((row & 3u) << 1) | ((row >> 3) & 1u);
-            return (((pos >> 1) ^ f) << 1) | (pos & 1u);
+// Position of granule `pos` of staged row `row` (and back: the swizzles are
+// their own inverses).
+template <bool T>
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t pos) {
+    if (T) {
+        const uint32_t f = ((row & 3u) << 1) | ((row >> 3) & 1u);
+        return (((pos >> 1) ^ f) << 1) | (pos & 1u);
+    }
+    return pos ^ ((row >> 1) & 7u);
+}
+
+// The loads of a stage of one operand by the 4 waves: kLoads instructions of
+// 1 KB each, wave w those from w kLoads on; instruction q covers the staged
+// rows [q kRows, (q + 1) kRows), 128-byte pieces or longer (with 64-byte
+// pieces L2 is asked twice as often and the address unit is busy twice as
+// long).  A lane's granule follows from the swizzle of its row, which takes
+// kKinds values over the instructions of a wave.
+template <int ROWS, bool T>
+struct Loader {
+    static constexpr int kLoads = ROWS * SK * 2 / 1024 / 4;
+    static constexpr int kPerRow = T ? ROWS / 8 : SK / 8;  // granules per staged row
+    static constexpr int kRows = 64 / kPerRow;
+    static constexpr int kKinds = T && ROWS == 256 ? 4 : 2;
+    __device__ __forceinline__ static constexpr int kind(int j) {
+        return !T ? j & 1 : ROWS == 256 ? (j & 1) | (j >> 2 & 1) << 1 : j >> 1 & 1;
+    }
+    uint32_t voff[kKinds];   // byte offset of the lane's granule in an instruction's rows
+    uint32_t whole[kKinds];  // T = false: the same without the contraction's end
+    uint32_t soff[kLoads], lds0;
+    i32x4 d;        // descriptor of the stage to load
+    int64_t rest;   // contraction elements of the tile from that stage on
+    uint32_t lds;
+
+    __device__ __forceinline__ void init(uint32_t ld2, uint32_t lds_base, int wave, int lane) {
+        const uint32_t row = (uint32_t)(lane / kPerRow), pos = (uint32_t)(lane % kPerRow);
+        const uint32_t row0 = (uint32_t)(wave * kLoads * kRows);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint32_t g = swizzled<T>(row0 + (uint32_t)(j * kRows) + row, pos);
+            voff[kind(j)] = whole[kind(j)] = row * ld2 + g * 16u;
+            soff[j] = uni((row0 + (uint32_t)(j * kRows)) * ld2);
         }
-        return pos ^ ((row >> 1) & 7u);
+        lds0 = uni(lds_base + (uint32_t)(wave * kLoads) * 1024u);
+    }
+    // Descriptor of a stage of `left` (1 .. SK) contraction elements at p;
+    // `wide`: valid tile rows.
+    __device__ __forceinline__ void aim(const void* p, uint32_t wide, uint32_t left, uint32_t ld2) {
+        d = descriptor(p, T ? (left - 1) * ld2 + wide * 2u : (wide - 1) * ld2 + left * 2u);
+        if (!T) {  // granules past the contraction's end
+            const uint32_t ld_row = (uint32_t)((threadIdx.x & 63) / kPerRow) * ld2;
+#pragma unroll
+            for (int k = 0; k < kKinds; ++k) voff[k] = whole[k] - ld_row < left * 2u ? whole[k] : kOut;
+        }
+    }
+    // The first stage of a tile; without one (wide = 0) an endless row of
+    // stages that end at once.
+    __device__ __forceinline__ void start(const void* p, uint32_t wide, int64_t k, uint32_t ld2) {
+        rest = k;
+        if (wide == 0 || k <= 0) {
+            d = descriptor(p, 0);
+            if (wide == 0) rest = INT64_MAX;
+        } else {
+            aim(p, wide, (uint32_t)(k < SK ? k : SK), ld2);
+        }
+    }
+    // On to the next stage; false at the tile's end.
+    __device__ __forceinline__ bool advance(uint32_t wide, uint32_t ld2) {
+        rest -= SK;
+        const uint64_t base = ((uint64_t)(uint32_t)d[1] << 32 | (uint32_t)d[0]) + (T ? SK * (uint64_t)ld2 : SK * 2u);
+        if (rest >= SK) {
+            d[0] = (int)(uint32_t)base;
+            d[1] = (int)(uint32_t)(base >> 32);
+            return true;
+        }
+        if (rest <= 0) return false;
+        aim((const void*)base, wide, (uint32_t)rest, ld2);
+        return true;
+    }
+    __device__ __forceinline__ void begin(int slot) {
+        lds = uni(lds0 + (uint32_t)slot * (ROWS * SK * 2));
+    }
+    // instruction j of the wave
+    // instruction J of the wave
+    template <int J>
+    __device__ __forceinline__ void load() {
+        load_to_lds<J * 1024>(d, voff[kind(J)], soff[J], lds);
+    }
+    __device__ __forceinline__ void load(int j) {
+        if (j == 0) load<0>();
+        if (j == 1) load<1>();
+        if (j == 2) load<2>();
+        if (j == 3) load<3>();
+        if constexpr (kLoads == 8) {
+            if (j == 4) load<4>();
+            if (j == 5) load<5>();
+            if (j == 6) load<6>();
+            if (j == 7) load<7>();
+        }
     }
 };
 
-// Loads of one stage of an operand by one wave.
-template <int ROWS, int WAVES, bool T>
-__device__ __forceinline__ void issue_loads(const i32x4& rs, uint32_t ld2, uint32_t lds, int wave, int lane,
-                                            int left) {
-    using O = Operand<ROWS, WAVES, T>;
-    constexpr int per_row = T ? ROWS / 8 : 8;  // granules per staged row
-#pragma unroll
-    for (int j = 0; j < O::kLoads; ++j) {
-        const uint32_t q = (uint32_t)(wave * O::kLoads + j);
-        const uint32_t row = q * O::kRowsPerLoad + (uint32_t)(lane / per_row);
-        const uint32_t g = O::swizzled(row, (uint32_t)(lane % per_row));
-        uint32_t voff = (uint32_t)(lane / per_row) * ld2 + g * 16u;
-        if (!T && (int)(g * 8u) >= left) voff = kOut;  // past the contraction's end
-        load_to_lds(rs, voff, uni(q * O::kRowsPerLoad * ld2), uni(lds + q * 1024u));
-    }
-}
-
-// Fragment of tile rows [32 blk, 32 blk + 32), contraction step s: lane l
+// Fragment of tile rows [32 blk, 32 blk + 32), step s of a stage: lane l
 // holds row l % 32, contraction elements 8 (l / 32) .. + 7 of the step.
 template <int ROWS, bool T>
 struct Reader {
@@ -195,24 +286,25 @@ struct Tile {
     int32_t stages;       // at least 1
 };
 
-// Walks the tiles slot, slot + nwg, ... of a workgroup (wgrad, longest groups
-// first: alternating directions, which evens out the sums).
+// A workgroup's way through its tiles: those of the rounds r = 0 .. count - 1,
+// beginning at round `first` and going round.
 struct Walk {
-    int64_t tile;
-    int g;     // position in tile order
-    bool odd;
+    int r, left;  // the next tile's round; tiles left, that one included
+    int g;        // position in tile order, for the search of the tile's group
 };
 
 template <int MODE, int TM, int TN>
 struct Sched {
-    int64_t total;
+    int total;
     int nwg, slot;
     bool lpt;
     const int32_t* tile_end;  // LDS: inclusive prefix of tiles per position
     const int32_t* order;     // LDS: group at a position (lpt)
 
-    __device__ __forceinline__ static int64_t bound(const Args& p, int g) {
-        const int64_t v = p.offsets[g];
+    // (constant address space: a scalar load where g is uniform, which no
+    // wait for vector loads delays)
+    __device__ __forceinline__ static int64_t bound(const Args& p, int64_t g) {
+        const int64_t v = ((const __attribute__((address_space(4))) int32_t*)p.offsets)[g];
         return v < 0 ? 0 : (v > p.M ? p.M : v);
     }
     __device__ __forceinline__ static int64_t rows_of(const Args& p, int g) {
@@ -222,7 +314,7 @@ struct Sched {
 
     __device__ __forceinline__ Tile decode(const Args& p, Walk& w) const {
         Tile T;
-        if (w.tile >= total) {
+        if (w.left <= 0) {
             T.a = p.a;
             T.b = p.b;
             T.out = 0;
@@ -231,11 +323,12 @@ struct Sched {
             T.stages = 1;
             return T;
         }
-        while (tile_end[w.g] <= w.tile) ++w.g;
+        const int tile = tile_of(w.r);
+        while (tile_end[w.g] <= tile) ++w.g;
         w.g = (int)uni((uint32_t)w.g);
         const int first = w.g > 0 ? (int)uni((uint32_t)tile_end[w.g - 1]) : 0;
-        const uint32_t local = uni((uint32_t)(w.tile - first));
-        const int grp = lpt ? (int)uni((uint32_t)order[w.g]) : w.g;
+        const uint32_t local = uni((uint32_t)(tile - first));
+        const int grp = (int)uni((uint32_t)(lpt ? order[w.g] : w.g));
         const int64_t o0 = bound(p, grp), mg = rows_of(p, grp);
         const int64_t ilen = MODE == kWgrad ? p.I : mg;
         const uint32_t nI = (uint32_t)((ilen + TM - 1) / TM), nJ = (uint32_t)((p.J + TN - 1) / TN);
@@ -261,9 +354,29 @@ struct Sched {
         if (T.stages < 1) T.stages = 1;
         return T;
     }
+    // Round r of this workgroup: tile r nwg + slot; with the groups taken
+    // longest first, in alternating directions, which evens out the sums.
+    __device__ __forceinline__ int tile_of(int r) const {
+        return r * nwg + (lpt && (r & 1) ? nwg - 1 - slot : slot);
+    }
+    // Where groups are the contraction (wgrad), each XCD begins an eighth of
+    // its rounds after the one before: at any time they are in groups of
+    // different lengths, and do not all write their tiles at once.
+    __device__ __forceinline__ Walk begin(int xcd) const {
+        Walk w;
+        const int full = total / nwg;
+        w.left = full + (tile_of(full) < total ? 1 : 0);
+        w.r = MODE == kWgrad ? w.left * xcd / 8 : 0;
+        w.g = 0;
+        return w;
+    }
     __device__ __forceinline__ void next(Walk& w) const {
-        w.tile += !lpt ? nwg : (w.odd ? 2 * (int64_t)slot + 1 : 2 * (int64_t)(nwg - slot) - 1);
-        w.odd = !w.odd;
+        --w.left;
+        ++w.r;
+        if (MODE == kWgrad && tile_of(w.r) >= total) {
+            w.r = 0;
+            w.g = 0;
+        }
     }
 };
 
@@ -271,14 +384,26 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)y) << 16);
 }
 
+// Keeps the accumulators of row blocks i and on where the matrix instructions
+// leave them: otherwise all of them are copied out before the first store.
+template <int MI, int NJ>
+__device__ __forceinline__ void keep_acc(f32x16 (&acc)[MI][NJ], int i) {
+#pragma unroll
+    for (int k = 0; k < MI; ++k)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (k >= i) asm volatile("" : "+a"(acc[k][j]));
+}
+
 template <int MODE, int TM, int TN, int WM, int WN, int OUT>
-__global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, 2) void grouped_bf16_kernel(Args p) {
+__global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void grouped_bf16_kernel(Args p) {
     constexpr int kWaves = (TM / WM) * (TN / WN);
+    static_assert(kWaves == 4 && TM == TN, "each wave loads a quarter of both operands");
     constexpr int MI = WM / 32, NJ = WN / 32;
     constexpr bool TA = MODE == kWgrad, TB = MODE != kForward;
     constexpr int kThreads = kWaves * 64;
-    __shared__ __attribute__((aligned(16))) uint8_t lds_a[2][TM * SK * 2];
-    __shared__ __attribute__((aligned(16))) uint8_t lds_b[2][TN * SK * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a[kRing][TM * SK * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_b[kRing][TN * SK * 2];
     __shared__ int32_t part[kThreads];
     extern __shared__ int32_t table[];  // tile_end [G], then order [G] (wgrad, few groups)
 
@@ -335,41 +460,43 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, 2) void grouped_bf16_ke
             if (t * per + e < G) table[t * per + e] += before;
         __syncthreads();
     }
-    S.total = (int64_t)uni((uint32_t)table[G - 1]);
+    S.total = (int)uni((uint32_t)table[G - 1]);
     if (S.slot >= S.total) return;
+    const Walk start = S.begin(bid % 8);
 
     const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
-    const uint32_t la = lds_addr(lds_a[0]), lb = lds_addr(lds_b[0]);
     Reader<TM, TA> ra;
     Reader<TN, TB> rb;
     ra.init(wm * MI, MI, lane);
     rb.init(wn * NJ, NJ, lane);
+    Loader<TM, TA> qa;
+    Loader<TN, TB> qb;
+    qa.init(lda2, lds_addr(lds_a[0]), wave, lane);
+    qb.init(ldb2, lds_addr(lds_b[0]), wave, lane);
+    constexpr int kLoads = Loader<TM, TA>::kLoads;  // of each operand, per wave and stage
 
-    // The loads run up to two stages ahead of the products, over the ends of
-    // tiles: they have a walk of their own.
-    Walk lw{S.slot, 0, false}, cw{S.slot, 0, false};
+    // The loads run two stages ahead of the products, over the ends of tiles:
+    // they have a walk of their own.  A's go first; L is the tile they are in,
+    // and B follows a step later.
+    Walk lw = start, cw = start;
     Tile L = S.decode(p, lw);
-    int ls = 0;
-    auto issue = [&](int buf) {
-        if (L.rows > 0) {
-            const int64_t k0 = (int64_t)ls * SK;
-            const int left = (int)(L.k - k0 < SK ? L.k - k0 : SK);  // <= 0: an empty contraction
-            const uint32_t some = left > 0 ? 1u : 0u;
-            const uint32_t abytes = TA ? ((uint32_t)(left - 1) * lda2 + (uint32_t)L.rows * 2u)
-                                       : ((uint32_t)(L.rows - 1) * lda2 + (uint32_t)left * 2u);
-            const uint32_t bbytes = TB ? ((uint32_t)(left - 1) * ldb2 + (uint32_t)L.cols * 2u)
-                                       : ((uint32_t)(L.cols - 1) * ldb2 + (uint32_t)left * 2u);
-            const i32x4 da = descriptor(L.a + (TA ? k0 * p.lda : k0), some * abytes);
-            const i32x4 db = descriptor(L.b + (TB ? k0 * p.ldb : k0), some * bbytes);
-            issue_loads<TM, kWaves, TA>(da, lda2, la + (uint32_t)buf * (TM * SK * 2), wave, lane, left);
-            issue_loads<TN, kWaves, TB>(db, ldb2, lb + (uint32_t)buf * (TN * SK * 2), wave, lane, left);
-            if (++ls == L.stages) {
-                S.next(lw);
-                L = S.decode(p, lw);
-                ls = 0;
-            }
+    uint32_t bcols = (uint32_t)L.cols;
+    qa.start(L.a, (uint32_t)L.rows, L.k, lda2);
+    qb.start(L.b, (uint32_t)L.cols, L.k, ldb2);
+    auto advance_a = [&]() {
+        if (!qa.advance((uint32_t)L.rows, lda2)) {
+            S.next(lw);
+            L = S.decode(p, lw);
+            qa.start(L.a, (uint32_t)L.rows, L.k, lda2);
         }
     };
+    auto advance_b = [&]() {
+        if (!qb.advance(bcols, ldb2)) {
+            bcols = (uint32_t)L.cols;
+            qb.start(L.b, bcols, L.k, ldb2);
+        }
+    };
+
     f32x16 acc[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -379,44 +506,72 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, 2) void grouped_bf16_ke
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     bf16x8 fa[2][MI], fb[2][NJ];
-    auto read = [&](int set, int buf, int s) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[set][i] = ra.read(lds_a[buf], i, s);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[set][j] = rb.read(lds_b[buf], j, s);
+    // fragment f of step k of a stage, B's first: a step's products begin with them
+    auto read = [&](int slot, int k, int f) {
+        if (f < NJ) fb[k & 1][f] = rb.read(lds_b[slot], f, k);
+        else fa[k & 1][f - NJ] = ra.read(lds_a[slot], f - NJ, k);
     };
+    // Step k of a stage: its products, and between them the reads of the next
+    // step (from ring slot rslot) and loads into slot lslot: A's of a stage in
+    // the last step of a stage, B's of the same stage in the first step of the
+    // next one.
+    // The empty statements keep this order: the compiler would otherwise
+    // gather the reads next to their first use.
     // B rows as the instruction's rows and A rows as its columns: a lane then
-    // holds 4 consecutive output columns of one output row
-    auto multiply = [&](int set) {
+    // holds 4 consecutive output columns of one output row.
+    auto step = [&](auto which, int rslot, int lslot) {
+        constexpr int k = decltype(which)::value, set = k & 1;
+        constexpr int kMul = MI * NJ, kReads = MI + NJ;
+        if (k == kSteps - 1) qa.begin(lslot);
+        if (k == 0) qb.begin(lslot);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int m = 0; m < kMul; ++m) {
+            const int i = m / NJ, j = m % NJ;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+            for (int f = 0; f < kReads; ++f)
+                if (f * kMul * 5 / 8 / kReads == m) read(rslot, (k + 1) % kSteps, f);
+#pragma unroll
+            for (int q = kLoads * m / kMul; q < kLoads * (m + 1) / kMul; ++q) {
+                if (k == kSteps - 1) qa.load(q);
+                if (k == 0) qb.load(q);
+            }
+            if (m + 1 < kMul) asm volatile("" : "+v"(fb[set][j]), "+v"(fa[set][(m + 1) / NJ]) : : "memory");
+        }
     };
 
-    issue(0);
-    issue(1);
-    wait_loads<0>();
-    __syncthreads();
-    read(0, 0, 0);
+    // stages 0 and 1 but for B's part of the latter, which the first step loads
+    qa.begin(0);
+    qb.begin(0);
+#pragma unroll
+    for (int m = 0; m < kLoads; ++m) {
+        qa.load(m);
+        qb.load(m);
+    }
+    advance_a();
+    advance_b();
+    qa.begin(1);
+#pragma unroll
+    for (int m = 0; m < kLoads; ++m) qa.load(m);
+    wait_loads<kLoads>();
+    meet();
+#pragma unroll
+    for (int f = 0; f < MI + NJ; ++f) read(0, 0, f);
 
     Tile C = S.decode(p, cw);
-    int buf = 0;
+    int slot = 0;
     while (C.rows > 0) {
         for (int s = 0; s < C.stages; ++s) {
-            read(1, buf, 1);
-            multiply(0);
-            read(0, buf, 2);
-            multiply(1);
-            read(1, buf, 3);
-            multiply(0);
+            step(std::integral_constant<int, 0>(), slot, slot ^ 1);
+            advance_a();
+            step(std::integral_constant<int, 1>(), slot, 0);
+            advance_b();
+            step(std::integral_constant<int, 2>(), slot, 0);
+            // the next stage has landed, and every wave has read this one
             wait_loads<0>();
-            __syncthreads();
-            issue(buf);
-            buf ^= 1;
-            read(0, buf, 0);
-            multiply(1);
+            meet();
+            step(std::integral_constant<int, 3>(), slot ^ 1, slot);
+            slot ^= 1;
         }
         // lane l: output row 32 i + l % 32 of the wave's part and, in element
         // 4 q + u, column 32 j + 8 q + 4 (l / 32) + u
@@ -427,6 +582,7 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, 2) void grouped_bf16_ke
             const rsrc_t rs = out_rsrc(out, (uint32_t)(C.rows - 1) * ldo2 + (uint32_t)C.cols * 2u);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
+                keep_acc<MI, NJ>(acc, i);
                 const int row = wm * WM + i * 32 + r32;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
@@ -441,29 +597,44 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, 2) void grouped_bf16_ke
                         const auto sy = __builtin_amdgcn_permlane32_swap(y0, y1, false, false);
                         const int col = wn * WN + j * 32 + 8 * q + 8 * h;
                         const uint32_t off = row < C.rows && col < C.cols ? (uint32_t)row * ldo2 + (uint32_t)col * 2u
-                                                                         : kOut;
+                                                                         : kOutStore;
                         __builtin_amdgcn_raw_buffer_store_b128(
                             u32x4{(uint32_t)sx[0], (uint32_t)sy[0], (uint32_t)sx[1], (uint32_t)sy[1]}, rs, (int)off, 0,
                             0);
                     }
             }
         } else {
-            float* const out = (float*)p.out + C.out;
+            // in pieces of two blocks, the values added to read a piece ahead
             const uint32_t ldo4 = (uint32_t)p.ldo * 4u;
+            const rsrc_t rs = out_rsrc((float*)p.out + C.out, (uint32_t)(C.rows - 1) * ldo4 + (uint32_t)C.cols * 4u);
+            constexpr int kPieces = MI * NJ / 2;
+            u32x4 old[2][2][4];
+            const auto at = [&](int c, int j, int q) {
+                const int row = wm * WM + (c * 2 / NJ) * 32 + r32, col = wn * WN + (c * 2 % NJ + j) * 32 + 8 * q + 4 * h;
+                return (int)(row < C.rows && col < C.cols ? (uint32_t)row * ldo4 + (uint32_t)col * 4u : kOutStore);
+            };
+            const auto fetch = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int row = wm * WM + i * 32 + r32;
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                    for (int q = 0; q < 4; ++q)
+                        old[c & 1][j][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, at(c, j, q), 0, 0);
+            };
+            if (OUT == kFp32Add) fetch(0);
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+                keep_acc<MI, NJ>(acc, c * 2 / NJ);
+                __builtin_amdgcn_sched_barrier(0);  // (all reads at once would not fit in registers)
+                if (OUT == kFp32Add && c + 1 < kPieces) fetch(c + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int col = wn * WN + j * 32 + 8 * q + 4 * h;
-                        if (row < C.rows && col < C.cols) {
-                            f32x4* const d = (f32x4*)((char*)out + ((uint64_t)((uint32_t)row * (uint64_t)ldo4) + (uint32_t)col * 4u));
-                            f32x4 v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                            if (OUT == kFp32Add) v += *d;
-                            *d = v;
-                        }
+                        const f32x16& x = acc[c * 2 / NJ][c * 2 % NJ + j];
+                        f32x4 v{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                        if (OUT == kFp32Add) v += __builtin_bit_cast(f32x4, old[c & 1][j][q]);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at(c, j, q), 0, 0);
                     }
             }
         }
@@ -508,7 +679,7 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     const int64_t big = tile_bound<MODE>(p, 256, 256);
     if (big >= n) {
         const int64_t nwg = big < n ? big : n;
-        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 64, OUT>), dim3((unsigned)nwg), dim3(512), table,
+        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 128, OUT>), dim3((unsigned)nwg), dim3(256), table,
                            stream, p);
     } else {
         const int64_t small = tile_bound<MODE>(p, 128, 128);
