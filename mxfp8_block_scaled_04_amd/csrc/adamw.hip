@@ -13,13 +13,19 @@
 // keep their ratio to it.  Codes of v > 0 are never zero: m / eps would
 // follow in a later step.
 //
-// What bounds it: HBM.  Nothing is read twice; per element 12 to 30 bytes
-// move and about 50 vector operations run (the vector units could run about
-// 180 in the time of 28 bytes).
+// What bounds it: HBM, with about as much written as read.  Nothing is read
+// twice; per element 10 to 30 bytes move and 50 to 80 vector operations run
+// (the vector units could run 180 in the time of 28 bytes).  Measured on 48
+// tensors, 337 10^6 elements: float32 states, float32 masters, bf16 weights
+// and gradients (28 bytes) 1.74-1.79 ms, 5.3 TB/s; 8-bit states, float32
+// gradients (18 bytes) 1.16 ms, 5.2 TB/s; the norm of bf16 gradients 0.21 ms
+// right after a step, whose written data then leaves the caches.  96 short
+// tensors (115 10^3 elements): 8-11 us a step, 6.5 us the norm, latency.
 //
 // Layout: one launch for all tensors.  The plan cuts every tensor into
 // chunks of 4096 elements and names the tensor of each; workgroups of 4
-// waves take chunks with a stride of the grid.  A wave takes 256 consecutive
+// waves take chunks with a stride of the grid, reading the plan ahead and all
+// of a chunk before they store any of it.  A wave takes 256 consecutive
 // elements at a time, 4 per lane, so that every load and store of a wave is
 // one contiguous piece (256 B of codes to 1 KB of floats) and a block of an
 // 8-bit state is exactly one wave: its maximum is a reduction in registers.
@@ -43,7 +49,7 @@ struct Step {
     float c;          // factor of the gradients
     float b1, a1;     // beta1, 1 - beta1
     float b2, a2;     // beta2, 1 - beta2
-    float lr;
+    double lr;
     float size;       // lr / (1 - beta1^t)
     float root;       // 1 / sqrt(1 - beta2^t)
     float eps;
@@ -152,31 +158,21 @@ constexpr float kLeast = 0x1p-9f;   // smallest E4M3 value
 // up); a NaN passes.
 __device__ __forceinline__ float in_range(float y) { return y > kTop ? kTop : (y < -kTop ? -kTop : y); }
 
-// One chunk of one tensor.  W: 0 float32 weights, 1 bf16 weights with
-// float32 masters, 2 bf16 weights alone.
+// A block's values in a lane, as they are in memory.
 template <int W, bool GB, bool S8>
-__device__ __forceinline__ void step_chunk(const mx_adamw_tensor& t, int64_t chunk, const Step& s, int wave, int lane) {
-    typedef typename std::conditional<GB, uint16_t, float>::type grad_t;
-    const grad_t* const gp = (const grad_t*)t.g;
-    const bool vec = (t.types & kAdamwAligned) != 0;
-    const float keep = 1.0f - s.lr * t.weight_decay;
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-        const int64_t block = chunk * (kAdamwChunk / MX_ADAMW_BLOCK) + u * 4 + wave;
-        const int64_t first = block * MX_ADAMW_BLOCK;
-        if (first >= t.n) break;  // the same in every lane of the wave
-        const int64_t i = first + lane * kPer;
-        const int64_t left = t.n - i;
-        const int live = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-        const bool fast = vec && live == 4;
-        float g[4], m[4], v[4], w[4];
-        load4(gp, i, live, fast, g);
-        float ms = 0.0f, vs = 0.0f;
+struct Block {
+    float g[4], m[4], v[4], w[4];
+    uint32_t mc, vc;
+    float ms, vs;
+
+    __device__ __forceinline__ void load(const mx_adamw_tensor& t, int64_t block, int64_t i, int live, bool fast) {
+        typedef typename std::conditional<GB, uint16_t, float>::type grad_t;
+        load4((const grad_t*)t.g, i, live, fast, g);
         if (S8) {
             ms = t.m_scale[block];
             vs = t.v_scale[block];
-            decode4(load_codes((const uint8_t*)t.m, i, live, fast), m);
-            decode4(load_codes((const uint8_t*)t.v, i, live, fast), v);
+            mc = load_codes((const uint8_t*)t.m, i, live, fast);
+            vc = load_codes((const uint8_t*)t.v, i, live, fast);
         } else {
             load4((const float*)t.m, i, live, fast, m);
             load4((const float*)t.v, i, live, fast, v);
@@ -184,6 +180,18 @@ __device__ __forceinline__ void step_chunk(const mx_adamw_tensor& t, int64_t chu
         if (W == 0) load4((const float*)t.w, i, live, fast, w);
         if (W == 1) load4(t.master, i, live, fast, w);
         if (W == 2) load4((const uint16_t*)t.w, i, live, fast, w);
+    }
+
+    __device__ __forceinline__ void step_and_store(const mx_adamw_tensor& t, const Step& s, float keep, int64_t block,
+                                                   int64_t i, int live, bool fast, int lane) {
+        // every operation rounded by itself: which of them would be fused is
+        // the compiler's choice otherwise, and a code of the next step could
+        // hang on it
+#pragma clang fp contract(off)
+        if (S8) {
+            decode4(mc, m);
+            decode4(vc, v);
+        }
         float r[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -193,41 +201,83 @@ __device__ __forceinline__ void step_chunk(const mx_adamw_tensor& t, int64_t chu
                 v[e] *= v[e];
             }
             const float x = g[e] * s.c;
-            m[e] = fmaf(s.b1, m[e], s.a1 * x);
-            v[e] = fmaf(s.b2, v[e], s.a2 * x * x);
+            m[e] = s.b1 * m[e] + s.a1 * x;
+            v[e] = s.b2 * v[e] + s.a2 * (x * x);
             r[e] = __builtin_sqrtf(v[e]);
-            const float update = m[e] / fmaf(r[e], s.root, s.eps);
-            w[e] = fmaf(-s.size, update, keep * w[e]);
+            const float update = m[e] / (r[e] * s.root + s.eps);
+            w[e] = keep * w[e] - s.size * update;
         }
         if (W == 0) store4((float*)t.w, i, live, fast, w);
         if (W == 1) store4(t.master, i, live, fast, w);
         if (W != 0) store4((uint16_t*)t.w, i, live, fast, w);
-        if (S8) {
-            float am = 0.0f, av = 0.0f;  // (lanes past the end hold zeros)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                am = fmaxf(am, fabsf(m[e]));
-                av = fmaxf(av, r[e]);
-            }
-            am = fmaxf(wave_max(am), kTiny);
-            av = fmaxf(wave_max(av), kTiny);
-            const float im = kTop / am, iv = kTop / av;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                m[e] = in_range(m[e] * im);
-                const float y = in_range(r[e] * iv);
-                v[e] = r[e] > 0.0f && y < kLeast ? kLeast : y;
-            }
-            store_codes((uint8_t*)t.m, i, live, fast, encode4(m));
-            store_codes((uint8_t*)t.v, i, live, fast, encode4(v));
-            if (lane == 0) {
-                t.m_scale[block] = am / kTop;
-                t.v_scale[block] = av / kTop;
-            }
-        } else {
+        if (!S8) {
             store4((float*)t.m, i, live, fast, m);
             store4((float*)t.v, i, live, fast, v);
+            return;
         }
+        float am = 0.0f, av = 0.0f;  // (lanes past the end hold zeros)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            am = fmaxf(am, fabsf(m[e]));
+            av = fmaxf(av, r[e]);
+        }
+        am = fmaxf(wave_max(am), kTiny);
+        av = fmaxf(wave_max(av), kTiny);
+        const float im = 1.0f / am * kTop, iv = 1.0f / av * kTop;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            m[e] = in_range(m[e] * im);
+            const float y = in_range(r[e] * iv);
+            v[e] = r[e] > 0.0f && y < kLeast ? kLeast : y;
+        }
+        store_codes((uint8_t*)t.m, i, live, fast, encode4(m));
+        store_codes((uint8_t*)t.v, i, live, fast, encode4(v));
+        if (lane == 0) {
+            t.m_scale[block] = am * (1.0f / kTop);
+            t.v_scale[block] = av * (1.0f / kTop);
+        }
+    }
+};
+
+// One chunk of one tensor.  W: 0 float32 weights, 1 bf16 weights with
+// float32 masters, 2 bf16 weights alone.  A whole aligned chunk reads all of
+// its blocks before it stores the first one (a load is not moved over a
+// store by itself: they could be to the same memory).
+template <int W, bool GB, bool S8>
+__device__ __forceinline__ void step_chunk(const mx_adamw_tensor& t, int64_t chunk, const Step& s, int wave, int lane) {
+    const float keep = (float)(1.0 - s.lr * (double)t.weight_decay);
+    const int64_t block0 = chunk * (kAdamwChunk / MX_ADAMW_BLOCK) + wave;
+    if ((t.types & kAdamwAligned) != 0 && (chunk + 1) * kAdamwChunk <= t.n) {
+        Block<W, GB, S8> b[kBlocks];
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+            b[u].load(t, block0 + 4 * u, (block0 + 4 * u) * MX_ADAMW_BLOCK + lane * kPer, 4, true);
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+            b[u].step_and_store(t, s, keep, block0 + 4 * u, (block0 + 4 * u) * MX_ADAMW_BLOCK + lane * kPer, 4, true,
+                                lane);
+        return;
+    }
+    // a tensor's end, or any alignment: the same, element by element where
+    // 4 do not exist or are not aligned
+    const bool vec = (t.types & kAdamwAligned) != 0;
+    Block<W, GB, S8> b[kBlocks];
+    const auto live_of = [&](int u) {
+        const int64_t left = t.n - (block0 + 4 * u) * MX_ADAMW_BLOCK - lane * kPer;
+        return left >= 4 ? 4 : (left > 0 ? (int)left : 0);
+    };
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t block = block0 + 4 * u;
+        if (block * MX_ADAMW_BLOCK < t.n)  // the same in every lane of the wave
+            b[u].load(t, block, block * MX_ADAMW_BLOCK + lane * kPer, live_of(u), vec && live_of(u) == 4);
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t block = block0 + 4 * u;
+        if (block * MX_ADAMW_BLOCK < t.n)
+            b[u].step_and_store(t, s, keep, block, block * MX_ADAMW_BLOCK + lane * kPer, live_of(u),
+                                vec && live_of(u) == 4, lane);
     }
 }
 
@@ -242,26 +292,48 @@ __device__ __forceinline__ void step_grad(const mx_adamw_tensor& t, int64_t chun
     else step_state<W, false>(t, chunk, s, wave, lane);
 }
 
+// The chunks k = first, first + stride, ... of a workgroup.  What the plan
+// says of a chunk is read ahead (its tensor two chunks ahead, the tensor's
+// entry one), by scalar loads: the plan is constant while a kernel runs.
+typedef const __attribute__((address_space(4))) AdamwEntry* entry_ptr;
+typedef const __attribute__((address_space(4))) int32_t* owner_ptr;
+template <typename F>
+__device__ __forceinline__ void for_chunks(const AdamwEntry* entries, const int32_t* owner, int64_t chunks, F work) {
+    const entry_ptr ep = (entry_ptr)entries;
+    const owner_ptr op = (owner_ptr)owner;
+    int64_t k = blockIdx.x;
+    const int64_t stride = gridDim.x;
+    if (k >= chunks) return;
+    const auto entry_of = [&](int32_t i) {
+        AdamwEntry e;
+        e.t.w = ep[i].t.w;
+        e.t.master = ep[i].t.master;
+        e.t.g = ep[i].t.g;
+        e.t.m = ep[i].t.m;
+        e.t.v = ep[i].t.v;
+        e.t.m_scale = ep[i].t.m_scale;
+        e.t.v_scale = ep[i].t.v_scale;
+        e.t.n = ep[i].t.n;
+        e.t.weight_decay = ep[i].t.weight_decay;
+        e.t.types = ep[i].t.types;
+        e.first_chunk = ep[i].first_chunk;
+        return e;
+    };
+    AdamwEntry e = entry_of(op[k]);
+    int32_t next = k + stride < chunks ? op[k + stride] : 0;
+    for (; k < chunks; k += stride) {
+        const AdamwEntry ahead = entry_of(next);
+        next = k + 2 * stride < chunks ? op[k + 2 * stride] : 0;
+        work(e.t, k - e.first_chunk);
+        e = ahead;
+    }
+}
+
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
-    __shared__ int64_t done;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const float c = a.grad_scale ? *a.grad_scale : 1.0f;
     const bool skip = !(c >= 0.0f && c <= __FLT_MAX__);
-    if (threadIdx.x == 0) {
-        // the count is read before the ticket is drawn, and the last
-        // workgroup to draw one raises it: every workgroup has read it then
-        const int64_t t = __hip_atomic_load(a.steps, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        done = t;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        const int64_t ticket = __hip_atomic_fetch_add(a.steps + 1, (int64_t)1, __ATOMIC_RELAXED,
-                                                      __HIP_MEMORY_SCOPE_AGENT);
-        if (ticket == (int64_t)gridDim.x - 1) {
-            __hip_atomic_store(a.steps + 1, (int64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (!skip) __hip_atomic_store(a.steps, t + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-    }
-    __syncthreads();
-    if (skip) return;
+    const int64_t done = *a.steps;
     const int64_t t = done + 1;
     Step s;
     s.c = c;
@@ -270,17 +342,27 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
     s.b2 = (float)a.beta2;
     s.a2 = (float)(1.0 - a.beta2);
     const double lr = a.lr_device ? (double)*a.lr_device : a.lr;
-    s.lr = (float)lr;
+    s.lr = lr;
     s.size = (float)(lr / (1.0 - power(a.beta1, t)));
     s.root = (float)(1.0 / sqrt(1.0 - power(a.beta2, t)));
     s.eps = (float)a.eps;
-    for (int64_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
-        const AdamwEntry* const e = a.entries + a.owner[k];
-        const mx_adamw_tensor tensor = e->t;
-        const int64_t chunk = k - e->first_chunk;
-        if (!(tensor.types & MX_ADAMW_W_BF16)) step_grad<0>(tensor, chunk, s, wave, lane);
-        else if (tensor.master) step_grad<1>(tensor, chunk, s, wave, lane);
-        else step_grad<2>(tensor, chunk, s, wave, lane);
+    if (!skip)
+        for_chunks(a.entries, a.owner, a.chunks, [&](const mx_adamw_tensor& tensor, int64_t chunk) {
+            if (!(tensor.types & MX_ADAMW_W_BF16)) step_grad<0>(tensor, chunk, s, wave, lane);
+            else if (tensor.master) step_grad<1>(tensor, chunk, s, wave, lane);
+            else step_grad<2>(tensor, chunk, s, wave, lane);
+        });
+    // Every wave has read the count when its workgroup draws a ticket here;
+    // the last workgroup to draw one raises it.
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        asm volatile("" ::"s"(done) : "memory");  // (the count is in a register by now)
+        const int64_t ticket = __hip_atomic_fetch_add(a.steps + 1, (int64_t)1, __ATOMIC_RELAXED,
+                                                      __HIP_MEMORY_SCOPE_AGENT);
+        if (ticket == (int64_t)gridDim.x - 1) {
+            __hip_atomic_store(a.steps + 1, (int64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (!skip) __hip_atomic_store(a.steps, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
     }
 }
 
@@ -288,17 +370,43 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
 // overflow there, and a sum over 10^9 elements keeps far more than the 24
 // bits of the result.
 template <typename T>
-__device__ __forceinline__ void norm_chunk(const mx_adamw_tensor& t, int64_t chunk, int wave, int lane, double& sum) {
-    const bool vec = (t.types & kAdamwAligned) != 0;
+__device__ __forceinline__ void norm_chunk(const mx_adamw_tensor& t, int64_t chunk, double& sum) {
+    constexpr int kWide = 16 / sizeof(T), kLoads = kAdamwChunk / (kThreads * kWide);
+    const T* const g = (const T*)t.g;
+    const int64_t first = chunk * kAdamwChunk;
+    const auto add = [&](float x) { sum = fma((double)x, (double)x, sum); };
+    if (((uintptr_t)g & 15) == 0 && first + kAdamwChunk <= t.n) {
+        uint4 x[kLoads];
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-        const int64_t i = chunk * kAdamwChunk + (u * 4 + wave) * MX_ADAMW_BLOCK + lane * kPer;
-        const int64_t left = t.n - i;
-        const int live = left >= 4 ? 4 : (left > 0 ? (int)left : 0);
-        float g[4];
-        load4((const T*)t.g, i, live, vec && live == 4, g);
+        for (int u = 0; u < kLoads; ++u) {
+            // (an ordinary load: what stays in the caches is read again by the step.  With a
+            // non-temporal one this kernel is 5 % faster and the step after it 2.5 % slower,
+            // 1.96 against 2.00 ms for both at 337 10^6 gradients)
+            x[u] = *(const uint4*)(g + first + (u * kThreads + threadIdx.x) * kWide);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum = fma((double)g[e], (double)g[e], sum);
+        for (int u = 0; u < kLoads; ++u)
+            for (uint32_t w : {x[u].x, x[u].y, x[u].z, x[u].w}) {
+                if (sizeof(T) == 4) {
+                    add(__builtin_bit_cast(float, w));
+                } else {
+                    add(__builtin_bit_cast(float, w << 16));
+                    add(__builtin_bit_cast(float, w & 0xFFFF0000u));
+                }
+            }
+        return;
+    }
+    constexpr int kEach = kAdamwChunk / kThreads;  // a tensor's end, or any alignment
+    T x[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int64_t i = first + u * kThreads + threadIdx.x;
+        x[u] = i < t.n ? g[i] : (T)0;
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        if constexpr (sizeof(T) == 4) add(x[u]);
+        else add(__builtin_bit_cast(float, (uint32_t)x[u] << 16));
     }
 }
 
@@ -317,13 +425,11 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const AdamwEntry* e
                                                              float* out) {
     __shared__ double part[4], part2[4];
     __shared__ bool last;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     double sum = 0.0;
-    for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-        const AdamwEntry* const e = entries + owner[k];
-        if (e->t.types & MX_ADAMW_G_BF16) norm_chunk<uint16_t>(e->t, k - e->first_chunk, wave, lane, sum);
-        else norm_chunk<float>(e->t, k - e->first_chunk, wave, lane, sum);
-    }
+    for_chunks(entries, owner, chunks, [&](const mx_adamw_tensor& t, int64_t chunk) {
+        if (t.types & MX_ADAMW_G_BF16) norm_chunk<uint16_t>(t, chunk, sum);
+        else norm_chunk<float>(t, chunk, sum);
+    });
     const double total = group_sum(sum, part);
     if (threadIdx.x == 0) {
         __hip_atomic_store(ws->part + blockIdx.x, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -339,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const AdamwEntry* e
         const double norm = sqrt(all);
         const float rounded = (float)norm;
         out[0] = rounded;
-        out[1] = rounded <= __FLT_MAX__ ? (norm > (double)max_norm ? (float)(max_norm / norm) : 1.0f)
+        out[1] = rounded <= __FLT_MAX__ ? fminf(1.0f / rounded * max_norm, 1.0f)
                                         : __builtin_nanf("");
         __hip_atomic_store(&ws->ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -348,7 +454,9 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const AdamwEntry* e
 }  // namespace
 
 hipError_t launch_adamw(const AdamwArgs& a, hipStream_t stream) {
-    const int64_t most = 2048;  // 8 workgroups of 4 waves on each of 256 CUs
+    // 32 workgroups per CU: with 8 (all of them resident at once) 3 % slower,
+    // the last chunks of the fastest ones leave the others' unread
+    const int64_t most = 8192;
     const unsigned grid = (unsigned)(a.chunks < 1 ? 1 : (a.chunks < most ? a.chunks : most));
     hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
