@@ -650,6 +650,129 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
     wait_loads<0>();
 }
 
+// ---- few rows --------------------------------------------------------------
+//
+// Forward product where groups have few rows (a token or some in generation):
+// bound by reading the weights of the groups that have any, once.  A
+// workgroup takes 16 columns of the output for up to 16 rows of one group;
+// its 8 waves share the contraction out in pieces of 4 steps of 32 and add
+// their sums up in LDS, in a fixed order.  v_mfma_f32_16x16x32_bf16 with the
+// weights as its rows: a lane reads 16 bytes of row l % 16, so that a load
+// takes 64 bytes of each of 16 rows, straight into registers, and the loads
+// of a piece are in flight while the one before is multiplied.  Columns and
+// rows past their ends read as zeros (descriptors), and so do contraction
+// indices past K.
+// Measured at N 4096, K 7168: 8 rows of 8 groups 79 us, 6.0 TB/s (128-row
+// tiles 119 us); 64 rows of 64 groups 386 us, 6.2 TB/s; one row 13 us (68 us).
+// 32 columns and 4 waves per workgroup: 86, 434 and 18 us.
+constexpr int kFewWaves = 8;
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args p) {
+    constexpr int kPiece = 4, WAVES = kFewWaves;
+    __shared__ f32x4 sums[WAVES][64];
+    __shared__ int32_t found[3];  // group, first row, rows
+    __shared__ int32_t part[WAVES];
+    const int t = threadIdx.x, wave = (int)uni((uint32_t)t >> 6), lane = t & 63;
+
+    // The workgroup's block of up to 16 rows: the blockIdx.y-th of all groups.
+    // Each thread counts the blocks of some groups; then a prefix over the
+    // threads.
+    {
+        if (t == 0) found[0] = -1;
+        const int per = (p.G + WAVES * 64 - 1) / (WAVES * 64);
+        const auto rows_at = [&](int g, int64_t& lo) {
+            lo = Sched<kForward, 256, 256>::bound(p, g);
+            const int64_t n = Sched<kForward, 256, 256>::bound(p, g + 1) - lo;
+            return n > 0 ? n : 0;
+        };
+        int mine = 0;
+        int64_t lo;
+        for (int e = 0; e < per; ++e)
+            if (t * per + e < p.G) mine += (int)((rows_at(t * per + e, lo) + 15) / 16);
+        int upto = mine;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
+        }
+        if (lane == 63) part[wave] = upto;
+        __syncthreads();
+        int at = upto - mine;
+        for (int w = 0; w < wave; ++w) at += part[w];
+        const int want = (int)blockIdx.y;
+        if (at <= want && want < at + mine)
+            for (int e = 0; e < per; ++e) {
+                if (t * per + e >= p.G) break;
+                const int64_t n = rows_at(t * per + e, lo);
+                const int blocks = (int)((n + 15) / 16);
+                if (want < at + blocks) {
+                    const int64_t first = (int64_t)(want - at) * 16;
+                    found[0] = t * per + e;
+                    found[1] = (int)(lo + first);
+                    found[2] = (int)(n - first < 16 ? n - first : 16);
+                    break;
+                }
+                at += blocks;
+            }
+        __syncthreads();
+    }
+    const int g = (int)uni((uint32_t)found[0]);
+    if (g < 0) return;
+    const int64_t row0 = (int64_t)uni((uint32_t)found[1]);
+    const int rows = (int)uni((uint32_t)found[2]);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int cols = (int)(p.J - n0 < 16 ? p.J - n0 : 16);
+    const uint32_t K = (uint32_t)p.K, lda2 = (uint32_t)p.lda * 2u;
+    const rsrc_t rw = out_rsrc((void*)(p.b + ((int64_t)g * p.J + n0) * p.K), (uint32_t)cols * K * 2u);
+    const rsrc_t rx = out_rsrc((void*)(p.a + row0 * p.lda), (uint32_t)(rows - 1) * lda2 + K * 2u);
+    const uint32_t r16 = (uint32_t)lane & 15u, k8 = ((uint32_t)lane >> 4) * 8u;
+
+    struct Piece {
+        bf16x8 w[kPiece], x[kPiece];
+    };
+    const auto fetch = [&](Piece& f, uint32_t piece) {
+#pragma unroll
+        for (int s = 0; s < kPiece; ++s) {
+            const uint32_t k = (piece * kPiece + (uint32_t)s) * 32u + k8;
+            const uint32_t xo = k < K ? r16 * lda2 + k * 2u : kOutStore;
+            const uint32_t wo = k < K ? r16 * K * 2u + k * 2u : kOutStore;
+            f.x[s] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)xo, 0, 0));
+            f.w[s] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)wo, 0, 0));
+        }
+    };
+    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto multiply = [&](const Piece& f) {
+#pragma unroll
+        for (int s = 0; s < kPiece; ++s)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[s], f.x[s], acc, 0, 0, 0);
+    };
+    const uint32_t pieces = (K + 32 * kPiece - 1) / (32 * kPiece);
+    if ((uint32_t)wave < pieces) {
+        Piece f0, f1;
+        fetch(f0, (uint32_t)wave);
+        for (uint32_t c = (uint32_t)wave;; c += 2 * WAVES) {
+            // (a piece past the end reads nothing: all of its indices are past K)
+            fetch(f1, c + WAVES);
+            multiply(f0);
+            if (c + WAVES >= pieces) break;
+            fetch(f0, c + 2 * WAVES);
+            multiply(f1);
+            if (c + 2 * WAVES >= pieces) break;
+        }
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    // lane l: output row l % 16, columns 4 (l / 16) .. + 3
+    if (wave == 0) {
+        f32x4 v = sums[0][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v += sums[w][lane];
+        const int col = 4 * (lane >> 4);
+        if ((int)r16 < rows && col < cols) {
+            uint16_t* const out = (uint16_t*)p.out + (row0 + r16) * p.ldo + n0 + col;
+            *(uint2*)out = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+        }
+    }
+}
+
 int cus() {
     static int cached[64] = {0};
     int dev = 0;
@@ -671,6 +794,13 @@ int64_t tile_bound(const Args& p, int64_t tm, int64_t tn) {
     const int64_t groups = p.G < p.M ? p.G : p.M;  // groups that can have rows
     return (tiles(p.M, tm) + groups) * tiles(p.J, tn);
 }
+
+// Whether a forward product goes to few_rows_kernel: on average at most 8 rows
+// a group (at 8, 128 rows of 16 groups at 4096 x 7168, both kernels take 198
+// us; at 4 it has 99 against 121 us, at 16 278 against 199), or few rows at
+// all (tiles would leave most CUs idle).  K: 16 rows of weights are a
+// descriptor's range.
+bool few_rows(const Args& p) { return p.M <= 8 * (int64_t)p.G || p.M <= 64; }
 
 template <int MODE, int OUT>
 hipError_t launch(const Args& p, hipStream_t stream) {
@@ -695,6 +825,12 @@ hipError_t launch(const Args& p, hipStream_t stream) {
 hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t G,
                                int64_t M, int64_t N, int64_t K, uint16_t* out, int64_t ldo, hipStream_t stream) {
     Args p = {x, w, offsets, out, ldx, K, ldo, M, 0, N, K, G};
+    if (few_rows(p)) {
+        const int64_t blocks = M < G + M / 16 ? M : G + M / 16;  // of 16 rows, at most
+        hipLaunchKernelGGL(few_rows_kernel, dim3((unsigned)tiles(N, 16), (unsigned)blocks), dim3(kFewWaves * 64), 0,
+                           stream, p);
+        return hipGetLastError();
+    }
     return launch<kForward, kBf16>(p, stream);
 }
 

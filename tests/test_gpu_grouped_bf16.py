@@ -26,6 +26,10 @@ CASES = [
     ([0, 0, 64], 72, 56),
     ([3] * 40, 40, 136),
 ]
+# at most 8 rows a group on average: blocks of 16 rows that end in a group, contractions that
+# end inside a piece of a wave (128), columns that end inside 16
+FEW = [([16], 24, 1032), ([17, 0, 1], 40, 4104), ([0, 33, 15, 2, 0, 0, 0, 0], 264, 136), ([1] * 9 + [0] * 300, 16, 8),
+       ([0, 0, 48], 8, 2056)]
 # every workgroup of the large-tile launch runs several tiles (full output checked)
 LARGE = [([1500, 0, 33, 2600, 900, 1, 511, 2047], 1288, 328)]
 
@@ -61,7 +65,7 @@ def _products(ends, a, b):
     return torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts])
 
 
-@pytest.mark.parametrize("sizes,N,K", CASES + LARGE)
+@pytest.mark.parametrize("sizes,N,K", CASES + FEW + LARGE)
 @pytest.mark.parametrize("pad", [0, 24])
 def test_forward(sizes, N, K, pad):
     ends, off = _setup(sizes)
