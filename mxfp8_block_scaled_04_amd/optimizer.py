@@ -1,0 +1,72 @@
+"""AdamW over a list of tensors: the states, the plan and the calls of
+mx_grad_norm and mx_adamw, kept together (include/libmxmoe_train.h for the
+arithmetic).  Nothing is read back by step(): it can be captured in a graph.
+"""
+import torch
+
+from .training import BLOCK, mx_adamw, mx_adamw_plan, mx_grad_norm
+
+
+class AdamW:
+    """weights: float32 or bf16 GPU tensors, updated in place by step();
+    grads: the tensors (float32 or bf16, same lengths) that hold their
+    gradients at every step.  bf16 weights get float32 masters unless
+    masters=False.  state_bits: 32, or 8 (E4M3 codes of m and sqrt(v) with a
+    float32 scale per 256 elements).  weight_decay: a number or one per
+    tensor.  max_norm: clip by the gradients' global norm; a step whose norm
+    is infinite or NaN then changes nothing."""
+
+    def __init__(self, weights, grads, lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, state_bits=32,
+                 masters=True, max_norm=None):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if not weights:
+            raise ValueError("no tensors")
+        self.weights, self.grads = list(weights), list(grads)
+        self.beta1, self.beta2 = betas
+        self.eps, self.max_norm = eps, max_norm
+        device = self.weights[0].device
+        self.lr = torch.tensor([lr], dtype=torch.float32, device=device)
+        self.steps = torch.zeros(2, dtype=torch.int64, device=device)
+        self.norm = torch.zeros(2, dtype=torch.float32, device=device)
+        self.masters = [w.float() if masters and w.dtype == torch.bfloat16 else None for w in self.weights]
+        kind = torch.float32 if state_bits == 32 else torch.uint8
+
+        def zeros(kind, length):
+            return [torch.zeros(length(w), dtype=kind, device=device) for w in self.weights]
+
+        self.m, self.v = (zeros(kind, lambda w: w.numel()) for _ in range(2))
+        self.m_scale, self.v_scale = (
+            (zeros(torch.float32, lambda w: -(-w.numel() // BLOCK)) for _ in range(2)) if state_bits == 8
+            else (None, None))
+        self.plan = mx_adamw_plan(self.weights, self.grads, self.m, self.v, masters=self.masters,
+                                  m_scales=self.m_scale, v_scales=self.v_scale, weight_decay=weight_decay)
+
+    def set_lr(self, lr):
+        self.lr.fill_(lr)
+
+    def step(self):
+        scale = None
+        if self.max_norm is not None:
+            scale = mx_grad_norm(self.plan, self.max_norm, out=self.norm)[1:]
+        mx_adamw(self.plan, self.steps, lr=self.lr, beta1=self.beta1, beta2=self.beta2, eps=self.eps,
+                 grad_scale=scale)
+
+    def _tensors(self):
+        lists = {"weights": self.weights, "masters": self.masters, "m": self.m, "v": self.v,
+                 "m_scale": self.m_scale or [], "v_scale": self.v_scale or []}
+        out = {f"{k}.{i}": t for k, ts in lists.items() for i, t in enumerate(ts) if t is not None}
+        return {**out, "steps": self.steps, "lr": self.lr}
+
+    def state_dict(self):
+        """Copies of everything that a later step depends on (weights too)."""
+        return {k: t.clone() for k, t in self._tensors().items()}
+
+    def load_state_dict(self, state):
+        """Into the tensors that are there: the plan stays valid."""
+        mine = self._tensors()
+        if set(state) != set(mine) or any(state[k].shape != t.shape or state[k].dtype != t.dtype
+                                          for k, t in mine.items()):
+            raise ValueError("the state is not of these tensors")
+        for k, t in mine.items():
+            t.copy_(state[k])
