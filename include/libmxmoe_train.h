@@ -57,11 +57,20 @@ mx_status mx_grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint
  *        values already there (MX_ERR_UNSUPPORTED for a bf16 dw: repeated
  *        rounding would lose the small ones).
  * A group without rows gives zeros (with accumulate: no change).
- * Requirements as above; dw_fp32 and accumulate are 0 or 1 (MX_ERR_SHAPE).
+ *   workspace  scratch memory of workspace_bytes, 16-byte aligned, or NULL: few
+ *        weights and long groups leave most of the GPU idle unless the rows
+ *        of a group are shared out and the parts' sums (fp32, kept here)
+ *        joined.  It is used if it has mx_grouped_gemm_bf16_wgrad_workspace_bytes
+ *        (0 where nothing would be shared out, -1 for invalid sizes); the
+ *        result differs by fp32 roundings.
+ * Requirements as above; dw_fp32 and accumulate are 0 or 1 and
+ * workspace_bytes >= 0 (MX_ERR_SHAPE).
  */
 mx_status mx_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,
                                      const int32_t* group_offsets, int32_t G, int64_t M, int64_t N, int64_t K,
-                                     void* dw, int32_t dw_fp32, int32_t accumulate, void* stream);
+                                     void* dw, int32_t dw_fp32, int32_t accumulate, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
+int64_t mx_grouped_gemm_bf16_wgrad_workspace_bytes(int32_t G, int64_t M, int64_t N, int64_t K);
 
 /* Types of a tensor of the optimizer (mx_adamw_tensor.types). */
 enum {

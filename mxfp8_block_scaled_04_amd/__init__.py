@@ -462,4 +462,4 @@ def mx_grouped_gemm_wgrad(A, As, B, Bs, padded_offsets, dW=None, stream=None):
 # The training step of unquantized experts (include/libmxmoe_train.h).
 from .training import (  # noqa: E402
     TRAIN_SYMBOLS, AdamWPlan, mx_adamw, mx_adamw_plan, mx_grad_norm, mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad,
-    mx_grouped_gemm_bf16_wgrad)
+    mx_grouped_gemm_bf16_wgrad, mx_grouped_gemm_bf16_wgrad_workspace_bytes)

@@ -74,16 +74,27 @@ mx_status mx_grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint
 
 mx_status mx_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,
                                      const int32_t* group_offsets, int32_t G, int64_t M, int64_t N, int64_t K,
-                                     void* dw, int32_t dw_fp32, int32_t accumulate, void* stream) {
+                                     void* dw, int32_t dw_fp32, int32_t accumulate, void* workspace,
+                                     int64_t workspace_bytes, void* stream) {
     const mx_status s = check_product(G, M, N, K, ldy, N, ldx, K);
     if (s != MX_OK) return s;
-    if ((dw_fp32 != 0 && dw_fp32 != 1) || (accumulate != 0 && accumulate != 1)) return MX_ERR_SHAPE;
+    if ((dw_fp32 != 0 && dw_fp32 != 1) || (accumulate != 0 && accumulate != 1) || workspace_bytes < 0)
+        return MX_ERR_SHAPE;
     if (accumulate && !dw_fp32) return MX_ERR_UNSUPPORTED;
     if (N == 0 || K == 0) return MX_OK;
     if (!group_offsets || !dw || (M > 0 && (!dy || !x))) return MX_ERR_NULL;
-    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(group_offsets, 4)) return MX_ERR_ALIGN;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(group_offsets, 4) ||
+        !aligned(workspace, 16))
+        return MX_ERR_ALIGN;
     return from_hip(mx::launch_grouped_bf16_wgrad(dy, ldy, x, ldx, group_offsets, G, M, N, K, dw, dw_fp32 != 0,
-                                                  accumulate != 0, (hipStream_t)stream));
+                                                  accumulate != 0, (float*)workspace, workspace_bytes,
+                                                  (hipStream_t)stream));
+}
+
+int64_t mx_grouped_gemm_bf16_wgrad_workspace_bytes(int32_t G, int64_t M, int64_t N, int64_t K) {
+    if (check_product(G, M, N, K, N, N, K, K) != MX_OK) return -1;
+    const int32_t split = mx::wgrad_split(G, M, N, K);
+    return split > 1 ? 4 * (int64_t)split * G * N * K : 0;
 }
 
 int64_t mx_adamw_plan_bytes(const mx_adamw_tensor* tensors, int32_t count) {

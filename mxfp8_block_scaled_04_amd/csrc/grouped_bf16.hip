@@ -75,7 +75,8 @@ struct Args {
     int64_t M;              // rows of the activations
     int64_t I, J;           // the output: [M][J] (I unused), wgrad [G][I][J]
     int64_t K;              // contraction length (wgrad: the group's rows)
-    int32_t G;
+    int32_t G;              // groups (wgrad: slices, `split` of each group)
+    int32_t split;          // wgrad: slices of each group's rows (1 otherwise)
 };
 
 __device__ __forceinline__ uint32_t uni(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -307,9 +308,25 @@ struct Sched {
         const int64_t v = ((const __attribute__((address_space(4))) int32_t*)p.offsets)[g];
         return v < 0 ? 0 : (v > p.M ? p.M : v);
     }
+    // First row and rows of a group, or of a slice of one: slices are whole
+    // stages long, the last ones of a group may be short or empty.
+    __device__ __forceinline__ static int64_t range_of(const Args& p, int g, int64_t& first) {
+        const int s = MODE == kWgrad && p.split > 1 ? g % p.split : 0;
+        const int grp = MODE == kWgrad && p.split > 1 ? g / p.split : g;
+        first = bound(p, grp);
+        int64_t n = bound(p, grp + 1) - first;
+        if (n < 0) n = 0;
+        if (MODE == kWgrad && p.split > 1) {
+            const int64_t len = ((n + p.split - 1) / p.split + SK - 1) / SK * SK;
+            const int64_t skip = s * len < n ? s * len : n;
+            first += skip;
+            n = n - skip < len ? n - skip : len;
+        }
+        return n;
+    }
     __device__ __forceinline__ static int64_t rows_of(const Args& p, int g) {
-        const int64_t n = bound(p, g + 1) - bound(p, g);
-        return n > 0 ? n : 0;
+        int64_t first;
+        return range_of(p, g, first);
     }
 
     __device__ __forceinline__ Tile decode(const Args& p, Walk& w) const {
@@ -329,7 +346,8 @@ struct Sched {
         const int first = w.g > 0 ? (int)uni((uint32_t)tile_end[w.g - 1]) : 0;
         const uint32_t local = uni((uint32_t)(tile - first));
         const int grp = (int)uni((uint32_t)(lpt ? order[w.g] : w.g));
-        const int64_t o0 = bound(p, grp), mg = rows_of(p, grp);
+        int64_t o0;
+        const int64_t mg = range_of(p, grp, o0);
         const int64_t ilen = MODE == kWgrad ? p.I : mg;
         const uint32_t nI = (uint32_t)((ilen + TM - 1) / TM), nJ = (uint32_t)((p.J + TN - 1) / TN);
         const uint32_t band = local / (kBand * nJ), r = local - band * (kBand * nJ);
@@ -807,7 +825,16 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     const unsigned table = 4u * (unsigned)p.G * (MODE == kWgrad && p.G <= kLptGroups ? 2u : 1u);
     const int64_t n = cus();
     const int64_t big = tile_bound<MODE>(p, 256, 256);
-    if (big >= n) {
+    // 256 x 256 tiles where they keep three quarters of the CUs busy (192
+    // tiles: 87 against 115 us at 2048 x 4096 x 4096, 4 groups; 128 tiles: 46
+    // against 33 us at 2048 x 2048 x 2048, 8 groups), unless the groups are
+    // as short as a small tile (64 rows a group on average, 4096 x 4096 x
+    // 4096: 457 against 435 us; 128 rows, 16384 x 2048 x 7168: 992 against 960)
+    // In wgrad, where a short contraction leaves the writing of the tiles to
+    // wait for: at least 4 tiles per CU (512 tiles, 256 rows a group: 41
+    // against 35 us; 1024 tiles: 63 against 64 us), or 1024 rows a group.
+    const bool fits = MODE == kWgrad ? big >= 4 * n || p.M >= 1024 * (int64_t)p.G : p.M > 128 * (int64_t)p.G;
+    if (big >= n * 3 / 4 && fits) {
         const int64_t nwg = big < n ? big : n;
         hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 128, OUT>), dim3((unsigned)nwg), dim3(256), table,
                            stream, p);
@@ -820,11 +847,30 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// out[g][i] = (out[g][i] +) the sum of the `split` slices' products, in order
+// of the slices; 4 elements per lane (n % 4 == 0).
+template <int OUT>
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int64_t n, int32_t split, void* out) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const float* const from = part + (int64_t)blockIdx.y * split * n + i;
+    f32x4 v = *(const f32x4*)from;
+    for (int s = 1; s < split; ++s) v += *(const f32x4*)(from + s * n);
+    const int64_t to = (int64_t)blockIdx.y * n + i;
+    if (OUT == kBf16) {
+        *(uint2*)((uint16_t*)out + to) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    } else {
+        f32x4* const d = (f32x4*)((float*)out + to);
+        if (OUT == kFp32Add) v += *d;
+        *d = v;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t G,
                                int64_t M, int64_t N, int64_t K, uint16_t* out, int64_t ldo, hipStream_t stream) {
-    Args p = {x, w, offsets, out, ldx, K, ldo, M, 0, N, K, G};
+    Args p = {x, w, offsets, out, ldx, K, ldo, M, 0, N, K, G, 1};
     if (few_rows(p)) {
         const int64_t blocks = M < G + M / 16 ? M : G + M / 16;  // of 16 rows, at most
         hipLaunchKernelGGL(few_rows_kernel, dim3((unsigned)tiles(N, 16), (unsigned)blocks), dim3(kFewWaves * 64), 0,
@@ -837,14 +883,41 @@ hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w
 hipError_t launch_grouped_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint16_t* w, const int32_t* offsets,
                                      int32_t G, int64_t M, int64_t N, int64_t K, uint16_t* dx, int64_t ldx,
                                      hipStream_t stream) {
-    Args p = {dy, w, offsets, dx, ldy, K, ldx, M, 0, K, N, G};
+    Args p = {dy, w, offsets, dx, ldy, K, ldx, M, 0, K, N, G, 1};
     return launch<kDgrad, kBf16>(p, stream);
+}
+
+// Slices of each group's rows: where small tiles leave workgroup slots empty
+// and the groups are long, so that a slice has 1024 rows or more on average
+// (65536 rows, 8 groups, 512 x 512: 8 slices 109 us, none 260 us).
+int32_t wgrad_split(int32_t G, int64_t M, int64_t N, int64_t K) {
+    const int64_t small = (int64_t)G * tiles(N, 128) * tiles(K, 128), slots = 512;
+    int64_t s = small > 0 ? slots / small : 1;
+    if (s > M / (1024 * (int64_t)G)) s = M / (1024 * (int64_t)G);
+    if (s > 32) s = 32;
+    return s < 2 ? 1 : (int32_t)s;
 }
 
 hipError_t launch_grouped_bf16_wgrad(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,
                                      const int32_t* offsets, int32_t G, int64_t M, int64_t N, int64_t K, void* dw,
-                                     bool fp32, bool accumulate, hipStream_t stream) {
-    Args p = {dy, x, offsets, dw, ldy, ldx, K, M, N, K, 0, G};
+                                     bool fp32, bool accumulate, float* workspace, int64_t workspace_bytes,
+                                     hipStream_t stream) {
+    Args p = {dy, x, offsets, dw, ldy, ldx, K, M, N, K, 0, G, 1};
+    const int32_t split = wgrad_split(G, M, N, K);
+    if (split > 1 && workspace && workspace_bytes >= 4 * (int64_t)split * G * N * K) {
+        p.out = workspace;
+        p.G = G * split;
+        p.split = split;
+        const hipError_t e = launch<kWgrad, kFp32>(p, stream);
+        if (e != hipSuccess) return e;
+        const int64_t n = N * K;
+        const dim3 grid((unsigned)tiles(n, 1024), (unsigned)G);
+        if (!fp32) hipLaunchKernelGGL(join_kernel<kBf16>, grid, dim3(256), 0, stream, workspace, n, split, dw);
+        else if (accumulate)
+            hipLaunchKernelGGL(join_kernel<kFp32Add>, grid, dim3(256), 0, stream, workspace, n, split, dw);
+        else hipLaunchKernelGGL(join_kernel<kFp32>, grid, dim3(256), 0, stream, workspace, n, split, dw);
+        return hipGetLastError();
+    }
     if (!fp32) return launch<kWgrad, kBf16>(p, stream);
     return accumulate ? launch<kWgrad, kFp32Add>(p, stream) : launch<kWgrad, kFp32>(p, stream);
 }

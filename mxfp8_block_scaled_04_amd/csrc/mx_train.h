@@ -50,6 +50,9 @@ hipError_t launch_grouped_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint
                                      hipStream_t stream);
 hipError_t launch_grouped_bf16_wgrad(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,
                                      const int32_t* offsets, int32_t G, int64_t M, int64_t N, int64_t K, void* dw,
-                                     bool fp32, bool accumulate, hipStream_t stream);
+                                     bool fp32, bool accumulate, float* workspace, int64_t workspace_bytes,
+                                     hipStream_t stream);
+// Slices that the rows of each group are cut into for it (1: none).
+int32_t wgrad_split(int32_t G, int64_t M, int64_t N, int64_t K);
 
 }  // namespace mx

@@ -18,8 +18,8 @@ W_BF16, G_BF16, STATE_8BIT = 1, 2, 4
 
 # Exported C symbols of include/libmxmoe_train.h, in its order.
 TRAIN_SYMBOLS = (
-    "mx_grouped_gemm_bf16", "mx_grouped_gemm_bf16_dgrad", "mx_grouped_gemm_bf16_wgrad", "mx_adamw_plan_bytes",
-    "mx_adamw_plan", "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw",
+    "mx_grouped_gemm_bf16", "mx_grouped_gemm_bf16_dgrad", "mx_grouped_gemm_bf16_wgrad",
+    "mx_grouped_gemm_bf16_wgrad_workspace_bytes", "mx_adamw_plan_bytes", "mx_adamw_plan", "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw",
 )
 
 
@@ -43,7 +43,8 @@ def _lib():
         for name, args, result in (
             ("mx_grouped_gemm_bf16", [P, I64, P, P, I32, I64, I64, I64, P, I64, P], ST),
             ("mx_grouped_gemm_bf16_dgrad", [P, I64, P, P, I32, I64, I64, I64, P, I64, P], ST),
-            ("mx_grouped_gemm_bf16_wgrad", [P, I64, P, I64, P, I32, I64, I64, I64, P, I32, I32, P], ST),
+            ("mx_grouped_gemm_bf16_wgrad", [P, I64, P, I64, P, I32, I64, I64, I64, P, I32, I32, P, I64, P], ST),
+            ("mx_grouped_gemm_bf16_wgrad_workspace_bytes", [I32, I64, I64, I64], I64),
             ("mx_adamw_plan_bytes", [P, I32], I64),
             ("mx_adamw_plan", [P, I32, P, P], ST),
             ("mx_grad_norm_workspace_bytes", [], I64),
@@ -130,10 +131,12 @@ def mx_grouped_gemm_bf16_dgrad(dy, w, group_offsets, dx=None, stream=None):
     return dx
 
 
-def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, stream=None):
+def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, workspace=None, stream=None):
     """dw[g] = sum over the rows r of group g of dy[r]^T x[r]: dy bf16 [M, N],
     x bf16 [M, K].  dw: a bf16 or float32 [G, N, K] tensor, or None (bf16 is
-    allocated); accumulate adds to the float32 dw given.  Returns dw."""
+    allocated); accumulate adds to the float32 dw given.  workspace: a uint8
+    tensor of mx_grouped_gemm_bf16_wgrad_workspace_bytes, allocated on the
+    stream's behalf if None.  Returns dw."""
     G = _offsets(group_offsets)
     ldy, ldx = _rows(dy, "dy"), _rows(x, "x")
     M, N = dy.shape
@@ -147,10 +150,23 @@ def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, 
     if tuple(dw.shape) != (G, N, K) or not dw.is_contiguous() or dw.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dw must be a contiguous bf16 or float32 [G, N, K] tensor")
     _same_device(dy, x, group_offsets, dw)
-    rc = _lib().mx_grouped_gemm_bf16_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(group_offsets), G, M, N, K, _ptr(dw),
-                                           int(dw.dtype == torch.float32), int(bool(accumulate)), _stream(stream))
+    lib = _lib()
+    if workspace is None:
+        size = lib.mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K)
+        if size > 0:  # from the pool of the stream that uses it: it can be given back before the call has run
+            with torch.cuda.stream(stream):  # (None: the current one)
+                workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dy.device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same GPU")
+    rc = lib.mx_grouped_gemm_bf16_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(group_offsets), G, M, N, K, _ptr(dw),
+                                        int(dw.dtype == torch.float32), int(bool(accumulate)), _ptr(workspace),
+                                        0 if workspace is None else workspace.numel(), _stream(stream))
     _check(rc, "mx_grouped_gemm_bf16_wgrad")
     return dw
+
+
+def mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K):
+    return int(_lib().mx_grouped_gemm_bf16_wgrad_workspace_bytes(int(G), int(M), int(N), int(K)))
 
 
 class AdamWPlan:

@@ -19,8 +19,9 @@ hipError_t launch_grouped_bf16_dgrad(const uint16_t*, int64_t, const uint16_t*, 
     return hipErrorNotSupported;
 }
 hipError_t launch_grouped_bf16_wgrad(const uint16_t*, int64_t, const uint16_t*, int64_t, const int32_t*, int32_t,
-                                     int64_t, int64_t, int64_t, void*, bool, bool, hipStream_t) {
+                                     int64_t, int64_t, int64_t, void*, bool, bool, float*, int64_t, hipStream_t) {
     return hipErrorNotSupported;
 }
+int32_t wgrad_split(int32_t, int64_t, int64_t, int64_t) { return 2; }
 
 }  // namespace mx

@@ -72,11 +72,13 @@ def test_product_refusals(name):
 
 
 def test_weight_gradient_refusals():
-    # (dy, ldy, x, ldx, offsets, G, M, N, K, dw, fp32, accumulate, stream)
-    f = _variants(T._lib().mx_grouped_gemm_bf16_wgrad, (FAKE, 64, FAKE, 72, FAKE, 4, 100, 64, 72, FAKE, 1, 1, None))
+    # (dy, ldy, x, ldx, offsets, G, M, N, K, dw, fp32, accumulate, workspace, bytes, stream)
+    f = _variants(T._lib().mx_grouped_gemm_bf16_wgrad,
+                  (FAKE, 64, FAKE, 72, FAKE, 4, 100, 64, 72, FAKE, 1, 1, FAKE, 64, None))
     assert f(a6=-1) == SHAPE and f(a7=60) == SHAPE and f(a8=70) == SHAPE
     assert f(a1=56) == SHAPE and f(a3=64) == SHAPE
-    assert f(a10=2) == SHAPE and f(a11=-1) == SHAPE
+    assert f(a10=2) == SHAPE and f(a11=-1) == SHAPE and f(a13=-1) == SHAPE
+    assert f(a12=P(0x100008)) == ALIGN
     assert f(a10=0) == UNSUPPORTED  # added to bf16
     for i in (0, 2, 4, 9):
         assert f(**{f"a{i}": None}) == NULL
@@ -85,6 +87,15 @@ def test_weight_gradient_refusals():
     assert f(a1=68) == ALIGN
     assert f(a7=0, a0=None, a9=None) == OK
     assert f(a6=0, a0=None, a2=None, a9=None) == NULL  # no rows: zeros are written
+
+
+def test_weight_gradient_workspace():
+    f = mx.mx_grouped_gemm_bf16_wgrad_workspace_bytes
+    assert f(0, 64, 8, 8) == -1 and f(1, -1, 8, 8) == -1 and f(1, 64, 12, 8) == -1
+    size = f(2, 65536, 256, 384)
+    assert size > 0 and size % (4 * 2 * 256 * 384) == 0
+    if not SAN:
+        assert f(16, 32768, 7168, 2048) == 0 and f(1, 128, 128, 128) == 0
 
 
 def _row(n=5, types=0, decay=0.0, w=0x1000, master=None, g=0x2000, m=0x3000, v=0x4000, ms=None, vs=None):

@@ -112,6 +112,36 @@ def test_wgrad(sizes, N, K, kind, pad):
         _check(got[g], ref, mag, e - s, kind == "bf16")
 
 
+# long groups and few weights: the rows shared out and joined, with slices that end short or empty
+SPLIT = [([3000], 8, 24), ([5000, 0, 1, 3400], 136, 72), ([129, 4000], 264, 200)]
+
+
+@pytest.mark.parametrize("sizes,N,K", SPLIT)
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "add"])
+def test_wgrad_shared_out(sizes, N, K, kind):
+    ends, off = _setup(sizes)
+    G, M = len(sizes), ends[-1]
+    need = mx.mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K)
+    assert need > 0
+    test_wgrad(sizes, N, K, kind, 24)
+    dy, x = _bf16((M, N), 5).cuda(), _bf16((M, K), 6).cuda()
+    outs = []
+    for size in (need, need, need - 1):  # a workspace that is too small is not used
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")  # NaN
+        dw = torch.ones((G, N, K), device="cuda", dtype=torch.bfloat16 if kind == "bf16" else torch.float32)
+        mx.mx_grouped_gemm_bf16_wgrad(dy, x, off, dw=dw, accumulate=kind == "add", workspace=ws[:size])
+        assert (ws[need:] == 255).all()
+        assert size == need or (ws == 255).all()
+        outs.append(dw)
+    assert torch.equal(outs[0], outs[1])
+    for g, (s, e) in enumerate(zip(ends, ends[1:])):
+        ref = dy[s:e].double().cpu().t() @ x[s:e].double().cpu()
+        mag = dy[s:e].double().cpu().abs().t() @ x[s:e].double().cpu().abs()
+        if kind == "add":
+            ref, mag = ref + 1, mag + 1
+        _check(outs[2][g], ref, mag, e - s, kind == "bf16")
+
+
 def test_rows_outside_the_groups_are_left_alone_and_malformed_offsets_stay_in_bounds():
     x, w = _bf16((300, 64), 8).cuda(), _bf16((3, 72, 64), 9).cuda()
     off = torch.tensor([10, 60, 60, 200], dtype=torch.int32, device="cuda")
