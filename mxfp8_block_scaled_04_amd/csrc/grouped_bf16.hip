@@ -17,7 +17,8 @@
 // 128 per wave) or two 128 x 128 tiles per CU (64 x 64 per wave),
 // v_mfma_f32_32x32x16_bf16.  A stage is 64 contraction elements of both
 // operands (64 KB for the large tile), loaded straight into LDS by 16-byte
-// direct loads; two stages in LDS.  A stage has 4 steps of 16: the fragments
+// direct loads; two stages in LDS (four for small tiles that have a CU to
+// themselves).  A stage has 4 steps of 16: the fragments
 // of a step are read while the one before is multiplied, also across stages
 // and tiles.  The wait for the next stage and the barrier sit before a
 // stage's last step, whose fragments are in registers by then; the loads of
@@ -43,7 +44,6 @@ namespace {
 
 constexpr int SK = 64;          // contraction elements per stage
 constexpr int kSteps = SK / 16;  // matrix instructions along it
-constexpr int kRing = 2;        // stages in LDS
 constexpr int kLptGroups = 512;  // wgrad: groups taken longest first up to this many
 constexpr int kBand = 4;         // row tiles per band of the tile order
 // An offset past every descriptor (fewer than 2^31 bytes: 256 rows of fewer
@@ -413,16 +413,17 @@ __device__ __forceinline__ void keep_acc(f32x16 (&acc)[MI][NJ], int i) {
             if (k >= i) asm volatile("" : "+a"(acc[k][j]));
 }
 
-template <int MODE, int TM, int TN, int WM, int WN, int OUT>
-__global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void grouped_bf16_kernel(Args p) {
+// RING: stages in LDS.
+template <int MODE, int TM, int TN, int WM, int WN, int OUT, int RING>
+__global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 2) void grouped_bf16_kernel(Args p) {
     constexpr int kWaves = (TM / WM) * (TN / WN);
     static_assert(kWaves == 4 && TM == TN, "each wave loads a quarter of both operands");
     constexpr int MI = WM / 32, NJ = WN / 32;
     constexpr bool TA = MODE == kWgrad, TB = MODE != kForward;
     constexpr int kThreads = kWaves * 64;
-    __shared__ __attribute__((aligned(16))) uint8_t lds_a[kRing][TM * SK * 2];
-    __shared__ __attribute__((aligned(16))) uint8_t lds_b[kRing][TN * SK * 2];
-    __shared__ int32_t part[kThreads];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_a[RING][TM * SK * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_b[RING][TN * SK * 2];
+    __shared__ int32_t part[kWaves];
     extern __shared__ int32_t table[];  // tile_end [G], then order [G] (wgrad, few groups)
 
     const int t = threadIdx.x, wave = (int)uni((uint32_t)t >> 6), lane = t & 63;
@@ -465,15 +466,15 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
             sum += (int32_t)tiles;
             table[g] = sum;
         }
-        part[t] = sum;
-        __syncthreads();
-        for (int d = 1; d < kThreads; d <<= 1) {
-            const int32_t v = t >= d ? part[t - d] : 0;
-            __syncthreads();
-            part[t] += v;
-            __syncthreads();
+        int32_t upto = sum;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
         }
-        const int32_t before = part[t] - sum;
+        if (lane == 63) part[wave] = upto;
+        __syncthreads();
+        int32_t before = upto - sum;
+        for (int w = 0; w < wave; ++w) before += part[w];
         for (int e = 0; e < per; ++e)
             if (t * per + e < G) table[t * per + e] += before;
         __syncthreads();
@@ -493,7 +494,7 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
     qb.init(ldb2, lds_addr(lds_b[0]), wave, lane);
     constexpr int kLoads = Loader<TM, TA>::kLoads;  // of each operand, per wave and stage
 
-    // The loads run two stages ahead of the products, over the ends of tiles:
+    // The loads run RING stages ahead of the products, over the ends of tiles:
     // they have a walk of their own.  A's go first; L is the tile they are in,
     // and B follows a step later.
     Walk lw = start, cw = start;
@@ -558,20 +559,22 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
         }
     };
 
-    // stages 0 and 1 but for B's part of the latter, which the first step loads
-    qa.begin(0);
-    qb.begin(0);
+    // the first RING stages but for B's part of the last one, which the first
+    // step loads
 #pragma unroll
-    for (int m = 0; m < kLoads; ++m) {
-        qa.load(m);
-        qb.load(m);
+    for (int k = 0; k < RING; ++k) {
+        qa.begin(k);
+#pragma unroll
+        for (int m = 0; m < kLoads; ++m) qa.load(m);
+        if (k + 1 < RING) {
+            qb.begin(k);
+#pragma unroll
+            for (int m = 0; m < kLoads; ++m) qb.load(m);
+            advance_a();
+            advance_b();
+        }
     }
-    advance_a();
-    advance_b();
-    qa.begin(1);
-#pragma unroll
-    for (int m = 0; m < kLoads; ++m) qa.load(m);
-    wait_loads<kLoads>();
+    wait_loads<(2 * RING - 3) * kLoads>();
     meet();
 #pragma unroll
     for (int f = 0; f < MI + NJ; ++f) read(0, 0, f);
@@ -580,16 +583,17 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
     int slot = 0;
     while (C.rows > 0) {
         for (int s = 0; s < C.stages; ++s) {
-            step(std::integral_constant<int, 0>(), slot, slot ^ 1);
+            const int next = (slot + 1) & (RING - 1);
+            step(std::integral_constant<int, 0>(), slot, (slot + RING - 1) & (RING - 1));
             advance_a();
             step(std::integral_constant<int, 1>(), slot, 0);
             advance_b();
             step(std::integral_constant<int, 2>(), slot, 0);
             // the next stage has landed, and every wave has read this one
-            wait_loads<0>();
+            wait_loads<(RING - 2) * 2 * kLoads>();
             meet();
-            step(std::integral_constant<int, 3>(), slot ^ 1, slot);
-            slot ^= 1;
+            step(std::integral_constant<int, 3>(), next, slot);
+            slot = next;
         }
         // lane l: output row 32 i + l % 32 of the wave's part and, in element
         // 4 q + u, column 32 j + 8 q + 4 (l / 32) + u
@@ -622,38 +626,33 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM == 256 ? 1 : 2) void
                     }
             }
         } else {
-            // in pieces of two blocks, the values added to read a piece ahead
+            // block by block, the values added to read a block ahead
             const uint32_t ldo4 = (uint32_t)p.ldo * 4u;
             const rsrc_t rs = out_rsrc((float*)p.out + C.out, (uint32_t)(C.rows - 1) * ldo4 + (uint32_t)C.cols * 4u);
-            constexpr int kPieces = MI * NJ / 2;
-            u32x4 old[2][2][4];
-            const auto at = [&](int c, int j, int q) {
-                const int row = wm * WM + (c * 2 / NJ) * 32 + r32, col = wn * WN + (c * 2 % NJ + j) * 32 + 8 * q + 4 * h;
+            u32x4 old[2][4];
+            const auto at = [&](int c, int q) {
+                const int row = wm * WM + (c / NJ) * 32 + r32, col = wn * WN + (c % NJ) * 32 + 8 * q + 4 * h;
                 return (int)(row < C.rows && col < C.cols ? (uint32_t)row * ldo4 + (uint32_t)col * 4u : kOutStore);
             };
             const auto fetch = [&](int c) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        old[c & 1][j][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, at(c, j, q), 0, 0);
+                for (int q = 0; q < 4; ++q)
+                    old[c & 1][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, at(c, q), 0, 0);
             };
             if (OUT == kFp32Add) fetch(0);
 #pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-                keep_acc<MI, NJ>(acc, c * 2 / NJ);
+            for (int c = 0; c < MI * NJ; ++c) {
+                keep_acc<MI, NJ>(acc, c / NJ);
                 __builtin_amdgcn_sched_barrier(0);  // (all reads at once would not fit in registers)
-                if (OUT == kFp32Add && c + 1 < kPieces) fetch(c + 1);
+                if (OUT == kFp32Add && c + 1 < MI * NJ) fetch(c + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x16& x = acc[c * 2 / NJ][c * 2 % NJ + j];
-                        f32x4 v{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-                        if (OUT == kFp32Add) v += __builtin_bit_cast(f32x4, old[c & 1][j][q]);
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at(c, j, q), 0, 0);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16& x = acc[c / NJ][c % NJ];
+                    f32x4 v{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                    if (OUT == kFp32Add) v += __builtin_bit_cast(f32x4, old[c & 1][q]);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at(c, q), 0, 0);
+                }
             }
         }
 #pragma unroll
@@ -836,12 +835,21 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     const bool fits = MODE == kWgrad ? big >= 4 * n || p.M >= 1024 * (int64_t)p.G : p.M > 128 * (int64_t)p.G;
     if (big >= n * 3 / 4 && fits) {
         const int64_t nwg = big < n ? big : n;
-        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 128, OUT>), dim3((unsigned)nwg), dim3(256), table,
+        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 128, OUT, 2>), dim3((unsigned)nwg), dim3(256),
+                           table, stream, p);
+        return hipGetLastError();
+    }
+    // 128 x 128 tiles, two workgroups per CU; with at most one per CU, four
+    // stages in LDS in place of two (the loads' latency is what bounds a
+    // workgroup that is alone)
+    const int64_t small = tile_bound<MODE>(p, 128, 128);
+    if (small > n) {
+        const int64_t nwg = small < 2 * n ? small : 2 * n;
+        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 128, 128, 64, 64, OUT, 2>), dim3((unsigned)nwg), dim3(256), table,
                            stream, p);
     } else {
-        const int64_t small = tile_bound<MODE>(p, 128, 128);
-        const int64_t nwg = small < 2 * n ? small : 2 * n;
-        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 128, 128, 64, 64, OUT>), dim3((unsigned)nwg), dim3(256), table,
+        const int64_t nwg = small < n ? small : n;
+        hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 128, 128, 64, 64, OUT, 4>), dim3((unsigned)nwg), dim3(256), table,
                            stream, p);
     }
     return hipGetLastError();

@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import _check, _ptr, _stream, load
+from . import _check, _ptr, load
 
 BLOCK = 256  # elements per scale of an 8-bit optimizer state
 
@@ -36,7 +36,7 @@ _signed = None
 def _lib():
     """The library, with the signatures of this module's calls set."""
     global _signed
-    lib = load()
+    lib = load()  # (another one if a program opens a build of its own)
     if _signed is not lib:
         P, I64, I32, F, D, ST = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double,
                                  ctypes.c_int)
@@ -57,34 +57,46 @@ def _lib():
     return lib
 
 
+# Small calls are bound by the host's part, so the checks below avoid what
+# costs a microsecond each (sets of devices, ctypes objects for addresses).
+_BF16, _INT32 = torch.bfloat16, torch.int32
+
+
+def _stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
 def _rows(t, name):
-    """Row stride of a bf16 [M, C] tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2:
+    """(rows, columns, row stride) of a bf16 matrix whose rows are contiguous."""
+    if t.dtype is not _BF16 or t.dim() != 2:
         raise TypeError(f"{name} must be a bf16 matrix")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    M, C = t.shape
+    ld, step = t.stride()
+    if C > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] <= 1 or t.shape[1] == 0:  # a stride that is not used
-        return 8 * -(-t.shape[1] // 8)
-    return t.stride(0)
+    if M <= 1 or C == 0:  # a stride that is not used
+        ld = 8 * -(-C // 8)
+    return M, C, ld
 
 
 def _offsets(t):
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < 2:
+    if t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < 2:
         raise ValueError("group_offsets must be a contiguous int32 [G + 1] tensor")
     return t.numel() - 1
 
 
 def _weights(w, G):
-    if w.dtype != torch.bfloat16 or w.dim() != 3 or not w.is_contiguous():
+    if w.dtype is not _BF16 or w.dim() != 3 or not w.is_contiguous():
         raise ValueError("w must be a contiguous bf16 [G, N, K] tensor")
-    if w.shape[0] != G:
+    g, N, K = w.shape
+    if g != G:
         raise ValueError("w and group_offsets differ in the number of groups")
-    return w.shape[1], w.shape[2]
+    return N, K
 
 
-def _same_device(*tensors):
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+def _same_device(first, *others):
+    at = first.get_device()  # -1: not on a GPU
+    if at < 0 or any(t is not None and t.get_device() != at for t in others):
         raise ValueError("all tensors must be on one GPU")
 
 
@@ -94,18 +106,17 @@ def mx_grouped_gemm_bf16(x, w, group_offsets, out=None, stream=None):
     Returns out bf16 [M, N]."""
     G = _offsets(group_offsets)
     N, K = _weights(w, G)
-    ldx = _rows(x, "x")
-    M = x.shape[0]
-    if x.shape[1] != K:
+    M, Kx, ldx = _rows(x, "x")
+    if Kx != K:
         raise ValueError("K mismatch")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    ldo = _rows(out, "out")
-    if tuple(out.shape) != (M, N):
+        out = torch.empty((M, N), dtype=_BF16, device=x.device)
+    Mo, No, ldo = _rows(out, "out")
+    if Mo != M or No != N:
         raise ValueError("out shape")
     _same_device(x, w, group_offsets, out)
-    rc = _lib().mx_grouped_gemm_bf16(_ptr(x), ldx, _ptr(w), _ptr(group_offsets), G, M, N, K, _ptr(out), ldo,
-                                     _stream(stream))
+    rc = _lib().mx_grouped_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), group_offsets.data_ptr(), G, M, N, K,
+                                     out.data_ptr(), ldo, _stream(stream))
     _check(rc, "mx_grouped_gemm_bf16")
     return out
 
@@ -115,18 +126,17 @@ def mx_grouped_gemm_bf16_dgrad(dy, w, group_offsets, dx=None, stream=None):
     [G, N, K].  Returns dx bf16 [M, K]."""
     G = _offsets(group_offsets)
     N, K = _weights(w, G)
-    ldy = _rows(dy, "dy")
-    M = dy.shape[0]
-    if dy.shape[1] != N:
+    M, Ny, ldy = _rows(dy, "dy")
+    if Ny != N:
         raise ValueError("N mismatch")
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
-    ldx = _rows(dx, "dx")
-    if tuple(dx.shape) != (M, K):
+        dx = torch.empty((M, K), dtype=_BF16, device=dy.device)
+    Mx, Kx, ldx = _rows(dx, "dx")
+    if Mx != M or Kx != K:
         raise ValueError("dx shape")
     _same_device(dy, w, group_offsets, dx)
-    rc = _lib().mx_grouped_gemm_bf16_dgrad(_ptr(dy), ldy, _ptr(w), _ptr(group_offsets), G, M, N, K, _ptr(dx), ldx,
-                                           _stream(stream))
+    rc = _lib().mx_grouped_gemm_bf16_dgrad(dy.data_ptr(), ldy, w.data_ptr(), group_offsets.data_ptr(), G, M, N, K,
+                                           dx.data_ptr(), ldx, _stream(stream))
     _check(rc, "mx_grouped_gemm_bf16_dgrad")
     return dx
 
@@ -138,29 +148,33 @@ def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, 
     tensor of mx_grouped_gemm_bf16_wgrad_workspace_bytes, allocated on the
     stream's behalf if None.  Returns dw."""
     G = _offsets(group_offsets)
-    ldy, ldx = _rows(dy, "dy"), _rows(x, "x")
-    M, N = dy.shape
-    K = x.shape[1]
-    if x.shape[0] != M:
+    M, N, ldy = _rows(dy, "dy")
+    Mx, K, ldx = _rows(x, "x")
+    if Mx != M:
         raise ValueError("dy and x differ in their rows")
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw = torch.empty((G, N, K), dtype=torch.bfloat16, device=x.device)
-    if tuple(dw.shape) != (G, N, K) or not dw.is_contiguous() or dw.dtype not in (torch.bfloat16, torch.float32):
+        dw = torch.empty((G, N, K), dtype=_BF16, device=x.device)
+    fp32 = dw.dtype is torch.float32
+    if tuple(dw.shape) != (G, N, K) or not dw.is_contiguous() or not (fp32 or dw.dtype is _BF16):
         raise ValueError("dw must be a contiguous bf16 or float32 [G, N, K] tensor")
-    _same_device(dy, x, group_offsets, dw)
+    _same_device(dy, x, group_offsets, dw, workspace)
     lib = _lib()
+    size = 0
     if workspace is None:
         size = lib.mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K)
         if size > 0:  # from the pool of the stream that uses it: it can be given back before the call has run
             with torch.cuda.stream(stream):  # (None: the current one)
                 workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dy.device:
-        raise ValueError("workspace must be a contiguous uint8 tensor on the same GPU")
-    rc = lib.mx_grouped_gemm_bf16_wgrad(_ptr(dy), ldy, _ptr(x), ldx, _ptr(group_offsets), G, M, N, K, _ptr(dw),
-                                        int(dw.dtype == torch.float32), int(bool(accumulate)), _ptr(workspace),
-                                        0 if workspace is None else workspace.numel(), _stream(stream))
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    else:
+        size = workspace.numel()
+    rc = lib.mx_grouped_gemm_bf16_wgrad(dy.data_ptr(), ldy, x.data_ptr(), ldx, group_offsets.data_ptr(), G, M, N, K,
+                                        dw.data_ptr(), fp32, bool(accumulate),
+                                        None if workspace is None else workspace.data_ptr(), max(size, 0),
+                                        _stream(stream))
     _check(rc, "mx_grouped_gemm_bf16_wgrad")
     return dw
 
@@ -177,6 +191,7 @@ class AdamWPlan:
         self.device, self.count, self.chunks, self.tensors = device, count, chunks, tensors
         self.image = image
         self.workspace = torch.zeros(int(_lib().mx_grad_norm_workspace_bytes()), dtype=torch.uint8, device=device)
+        self.address, self.workspace_address = image.data_ptr(), self.workspace.data_ptr()
 
 
 def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=None, weight_decay=0.0):
@@ -242,8 +257,8 @@ def mx_grad_norm(plan, max_norm=float("inf"), out=None, stream=None):
     if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 [2] tensor")
     _same_device(plan.image, out)
-    rc = _lib().mx_grad_norm(_ptr(plan.image), plan.count, plan.chunks, float(max_norm), _ptr(plan.workspace),
-                             _ptr(out), _stream(stream))
+    rc = _lib().mx_grad_norm(plan.address, plan.count, plan.chunks, max_norm, plan.workspace_address, out.data_ptr(),
+                             _stream(stream))
     _check(rc, "mx_grad_norm")
     return out
 
@@ -261,6 +276,7 @@ def mx_adamw(plan, steps, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None,
         if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
             raise ValueError(f"{name} must be a float32 tensor of one value")
     _same_device(plan.image, steps, on_device, grad_scale)
-    rc = _lib().mx_adamw(_ptr(plan.image), plan.count, plan.chunks, _ptr(steps), 0.0 if on_device is not None else lr,
-                         _ptr(on_device), beta1, beta2, eps, _ptr(grad_scale), _stream(stream))
+    rc = _lib().mx_adamw(plan.address, plan.count, plan.chunks, steps.data_ptr(), 0.0 if on_device is not None else lr,
+                         None if on_device is None else on_device.data_ptr(), beta1, beta2, eps,
+                         None if grad_scale is None else grad_scale.data_ptr(), _stream(stream))
     _check(rc, "mx_adamw")
