@@ -10,17 +10,19 @@
 // lies, 64 rows of the tile's width, and read with the transposing LDS read
 // (ds_read_b64_tr_b16), so that no transposed copy of anything is made.
 //
-// What bounds it: the matrix pipes, where groups have many rows; reading the
-// weights, where they have few.
+// What bounds it: with many rows a group the operand loads and the matrix
+// pipes, at the clock that the power limit leaves (forward, 32768 x 4096 x
+// 7168, 16 groups: 1.65 ms, 1.17 PFLOP/s, pipes busy 68 %; dgrad, 7168 x 2048:
+// 0.89 ms; wgrad of the same, added to fp32 values: 1.11 ms, of which the
+// values are 1.9 GB); with few rows reading the weights (few_rows_kernel).
 //
 // Layout: persistent workgroups of 4 waves, one 256 x 256 tile per CU (128 x
 // 128 per wave) or two 128 x 128 tiles per CU (64 x 64 per wave),
 // v_mfma_f32_32x32x16_bf16.  A stage is 64 contraction elements of both
 // operands (64 KB for the large tile), loaded straight into LDS by 16-byte
 // direct loads; two stages in LDS (four for small tiles that have a CU to
-// themselves).  A stage has 4 steps of 16: the fragments
-// of a step are read while the one before is multiplied, also across stages
-// and tiles.  The wait for the next stage and the barrier sit before a
+// themselves).  A stage has 4 steps of 16: the fragments of a step are read
+// while the one before is multiplied, also across stages and tiles.  The wait for the next stage and the barrier sit before a
 // stage's last step, whose fragments are in registers by then; the loads of
 // the stage after the next go into the buffer freed by that barrier, spread
 // over two steps.
@@ -77,6 +79,7 @@ struct Args {
     int64_t K;              // contraction length (wgrad: the group's rows)
     int32_t G;              // groups (wgrad: slices, `split` of each group)
     int32_t split;          // wgrad: slices of each group's rows (1 otherwise)
+    int32_t max_tiles;      // what valid offsets can give at most (malformed ones are cut off there)
 };
 
 __device__ __forceinline__ uint32_t uni(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -423,7 +426,7 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
     constexpr int kThreads = kWaves * 64;
     __shared__ __attribute__((aligned(16))) uint8_t lds_a[RING][TM * SK * 2];
     __shared__ __attribute__((aligned(16))) uint8_t lds_b[RING][TN * SK * 2];
-    __shared__ int32_t part[kWaves];
+    __shared__ int64_t part[kWaves];
     extern __shared__ int32_t table[];  // tile_end [G], then order [G] (wgrad, few groups)
 
     const int t = threadIdx.x, wave = (int)uni((uint32_t)t >> 6), lane = t & 63;
@@ -455,28 +458,29 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
         // tiles per position and their inclusive prefix
         const int64_t nJ = (p.J + TN - 1) / TN;
         const int per = (G + kThreads - 1) / kThreads;
-        int32_t sum = 0;
-        for (int e = 0; e < per; ++e) {
-            const int g = t * per + e;
-            if (g >= G) break;
+        const auto tiles_at = [&](int g) {
             const int64_t mg = S.rows_of(p, S.lpt ? order[g] : g);
             // a weight gradient without rows is zero: one empty stage, unless it is added to
-            const int64_t tiles = MODE == kWgrad ? (OUT == kFp32Add && mg == 0 ? 0 : (p.I + TM - 1) / TM * nJ)
-                                                 : (mg + TM - 1) / TM * nJ;
-            sum += (int32_t)tiles;
-            table[g] = sum;
-        }
-        int32_t upto = sum;
+            return MODE == kWgrad ? (OUT == kFp32Add && mg == 0 ? 0 : (p.I + TM - 1) / TM * nJ)
+                                  : (mg + TM - 1) / TM * nJ;
+        };
+        int64_t sum = 0;
+        for (int e = 0; e < per; ++e)
+            if (t * per + e < G) sum += tiles_at(t * per + e);
+        int64_t upto = sum;
         for (int d = 1; d < 64; d <<= 1) {
-            const int32_t v = __shfl_up(upto, d, 64);
+            const int64_t v = __shfl_up(upto, d, 64);
             if (lane >= d) upto += v;
         }
         if (lane == 63) part[wave] = upto;
         __syncthreads();
-        int32_t before = upto - sum;
-        for (int w = 0; w < wave; ++w) before += part[w];
+        int64_t so_far = upto - sum;
+        for (int w = 0; w < wave; ++w) so_far += part[w];
         for (int e = 0; e < per; ++e)
-            if (t * per + e < G) table[t * per + e] += before;
+            if (t * per + e < G) {
+                so_far += tiles_at(t * per + e);
+                table[t * per + e] = (int32_t)(so_far < p.max_tiles ? so_far : p.max_tiles);
+            }
         __syncthreads();
     }
     S.total = (int)uni((uint32_t)table[G - 1]);
@@ -820,7 +824,7 @@ int64_t tile_bound(const Args& p, int64_t tm, int64_t tn) {
 bool few_rows(const Args& p) { return p.M <= 8 * (int64_t)p.G || p.M <= 64; }
 
 template <int MODE, int OUT>
-hipError_t launch(const Args& p, hipStream_t stream) {
+hipError_t launch(Args p, hipStream_t stream) {
     const unsigned table = 4u * (unsigned)p.G * (MODE == kWgrad && p.G <= kLptGroups ? 2u : 1u);
     const int64_t n = cus();
     const int64_t big = tile_bound<MODE>(p, 256, 256);
@@ -833,7 +837,9 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     // wait for: at least 4 tiles per CU (512 tiles, 256 rows a group: 41
     // against 35 us; 1024 tiles: 63 against 64 us), or 1024 rows a group.
     const bool fits = MODE == kWgrad ? big >= 4 * n || p.M >= 1024 * (int64_t)p.G : p.M > 128 * (int64_t)p.G;
+    const auto most = [](int64_t tiles) { return (int32_t)(tiles < (1 << 30) ? tiles : 1 << 30); };
     if (big >= n * 3 / 4 && fits) {
+        p.max_tiles = most(big);
         const int64_t nwg = big < n ? big : n;
         hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 256, 256, 128, 128, OUT, 2>), dim3((unsigned)nwg), dim3(256),
                            table, stream, p);
@@ -843,6 +849,7 @@ hipError_t launch(const Args& p, hipStream_t stream) {
     // stages in LDS in place of two (the loads' latency is what bounds a
     // workgroup that is alone)
     const int64_t small = tile_bound<MODE>(p, 128, 128);
+    p.max_tiles = most(small);
     if (small > n) {
         const int64_t nwg = small < 2 * n ? small : 2 * n;
         hipLaunchKernelGGL((grouped_bf16_kernel<MODE, 128, 128, 64, 64, OUT, 2>), dim3((unsigned)nwg), dim3(256), table,
@@ -878,7 +885,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int64_t n,
 
 hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t G,
                                int64_t M, int64_t N, int64_t K, uint16_t* out, int64_t ldo, hipStream_t stream) {
-    Args p = {x, w, offsets, out, ldx, K, ldo, M, 0, N, K, G, 1};
+    Args p = {x, w, offsets, out, ldx, K, ldo, M, 0, N, K, G, 1, 0};
     if (few_rows(p)) {
         const int64_t blocks = M < G + M / 16 ? M : G + M / 16;  // of 16 rows, at most
         hipLaunchKernelGGL(few_rows_kernel, dim3((unsigned)tiles(N, 16), (unsigned)blocks), dim3(kFewWaves * 64), 0,
@@ -891,7 +898,7 @@ hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w
 hipError_t launch_grouped_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint16_t* w, const int32_t* offsets,
                                      int32_t G, int64_t M, int64_t N, int64_t K, uint16_t* dx, int64_t ldx,
                                      hipStream_t stream) {
-    Args p = {dy, w, offsets, dx, ldy, K, ldx, M, 0, K, N, G, 1};
+    Args p = {dy, w, offsets, dx, ldy, K, ldx, M, 0, K, N, G, 1, 0};
     return launch<kDgrad, kBf16>(p, stream);
 }
 
@@ -910,7 +917,7 @@ hipError_t launch_grouped_bf16_wgrad(const uint16_t* dy, int64_t ldy, const uint
                                      const int32_t* offsets, int32_t G, int64_t M, int64_t N, int64_t K, void* dw,
                                      bool fp32, bool accumulate, float* workspace, int64_t workspace_bytes,
                                      hipStream_t stream) {
-    Args p = {dy, x, offsets, dw, ldy, ldx, K, M, N, K, 0, G, 1};
+    Args p = {dy, x, offsets, dw, ldy, ldx, K, M, N, K, 0, G, 1, 0};
     const int32_t split = wgrad_split(G, M, N, K);
     if (split > 1 && workspace && workspace_bytes >= 4 * (int64_t)split * G * N * K) {
         p.out = workspace;

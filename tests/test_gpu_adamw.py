@@ -308,6 +308,34 @@ def test_8bit_states_follow_a_falling_gradient():
     assert ((got / v.sqrt() - 1).abs() < 0.15).all()
 
 
+def test_a_tensor_past_2_31_elements():
+    """8-bit states, bf16 weights and gradients, n > 2^31: the blocks at both
+    ends and around element 2^31 equal the same blocks stepped by themselves."""
+    n = 2 ** 31 + 3 * BLOCK + 5
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    base = torch.randn(1 << 20, generator=gen, device="cuda").bfloat16()
+    reps = -(-n // base.numel())
+    w, g = base.repeat(reps)[:n], base.flip(0).repeat(reps)[:n]
+    m, v = (torch.randint(1, 100, (1 << 20,), generator=gen, device="cuda", dtype=torch.uint8).repeat(reps)[:n]
+            for _ in range(2))
+    blocks = -(-n // BLOCK)
+    ms, vs = (torch.rand(blocks, generator=gen, device="cuda") * 1e-3 + 1e-6 for _ in range(2))
+    parts = []
+    for b in (0, 2 ** 31 // BLOCK - 2, 2 ** 31 // BLOCK, blocks - 2):
+        e, s = slice(b * BLOCK, min((b + 2) * BLOCK, n)), slice(b, min(b + 2, blocks))
+        parts.append((e, s, [t[e].clone() for t in (w, g, m, v)] + [t[s].clone() for t in (ms, vs)]))
+    plan = mx.mx_adamw_plan([w], [g], [m], [v], m_scales=[ms], v_scales=[vs], weight_decay=0.1)
+    mx.mx_adamw(plan, _steps(3), lr=1e-2)
+    for e, s, (pw, pg, pm, pv, pms, pvs) in parts:
+        one = mx.mx_adamw_plan([pw], [pg], [pm], [pv], m_scales=[pms], v_scales=[pvs], weight_decay=0.1)
+        mx.mx_adamw(one, _steps(3), lr=1e-2)
+        assert torch.equal(w[e], pw) and torch.equal(m[e], pm) and torch.equal(v[e], pv)
+        assert torch.equal(ms[s], pms) and torch.equal(vs[s], pvs)
+    out = mx.mx_grad_norm(plan)
+    norm = math.sqrt(sum(float(c.double().square().sum()) for c in g.split(1 << 28)))
+    assert abs(float(out[0]) - norm) <= 2 * U * norm
+
+
 def test_refusals():
     f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
     with pytest.raises(TypeError):

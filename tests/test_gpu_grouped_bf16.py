@@ -167,6 +167,44 @@ def test_infinite_and_nan_rows_stay_in_their_rows():
     assert not got.cpu()[~keep].isfinite().any()
 
 
+def test_malformed_offsets_with_many_overlapping_groups_end():
+    """Offsets that go back and forth make every other group the whole
+    matrix: the work is cut off at what valid offsets can give."""
+    G, M = 300, 4096
+    x, w = _bf16((M, 16), 20).cuda(), _bf16((G, 512, 16), 21).cuda()
+    off = torch.tensor([(g % 2) * M for g in range(G + 1)], dtype=torch.int32, device="cuda")
+    out = mx.mx_grouped_gemm_bf16(x, w, off)
+    mx.mx_grouped_gemm_bf16_dgrad(out, w, off)
+    mx.mx_grouped_gemm_bf16_wgrad(out, x, off)
+    torch.cuda.synchronize()
+
+
+def test_operands_past_2_31_elements_and_4_gib():
+    """x [300000, 8192] (4.9 GB): rows at both ends and around element 2^31
+    and byte 2^32, and the weight gradient of a group past them."""
+    M, K, N = 300000, 8192, 16
+    ends, off = _setup([100000, 200000 - 37, 37])
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    w, dy = _bf16((3, N, K), 23).cuda(), _bf16((M, N), 24).cuda()
+    out = mx.mx_grouped_gemm_bf16(x, w, off)
+    dx = mx.mx_grouped_gemm_bf16_dgrad(dy, w, off)
+    dw = mx.mx_grouped_gemm_bf16_wgrad(dy, x, off, dw=torch.empty((3, N, K), device="cuda"))
+    at = 2 ** 31 // K
+    for r in (0, 99990, at - 3, at + 3, M - 45, M - 8):
+        rows = slice(r, r + 8)
+        g = torch.tensor([sum(e <= i for e in ends[1:]) for i in range(r, r + 8)])
+        xr, dyr, wg = x[rows].double().cpu(), dy[rows].double().cpu(), w.double().cpu()[g]
+        _check(out[rows], (wg @ xr[:, :, None])[:, :, 0], (wg.abs() @ xr.abs()[:, :, None])[:, :, 0], K, True)
+        _check(dx[rows], (dyr[:, None] @ wg)[:, 0], (dyr.abs()[:, None] @ wg.abs())[:, 0], N, True)
+    last = slice(ends[2], M)
+    a, b = dy[last].double().cpu(), x[last].double().cpu()
+    _check(dw[2], a.t() @ b, a.abs().t() @ b.abs(), 37, False)
+    cols = slice(8184, 8192)
+    a, b = dy[ends[1]:ends[2]].double(), x[ends[1]:ends[2], cols].double()
+    _check(dw[1][:, cols], (a.t() @ b).cpu(), (a.abs().t() @ b.abs()).cpu(), ends[2] - ends[1], False)
+
+
 def test_empty_sizes():
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     w = _bf16((2, 16, 24), 12).cuda()
