@@ -290,11 +290,10 @@ struct Tile {
     int32_t stages;       // at least 1
 };
 
-// A workgroup's way through its tiles: those of the rounds r = 0 .. count - 1,
-// beginning at round `first` and going round.
+// A workgroup's way through its tiles, one in each round.
 struct Walk {
-    int r, left;  // the next tile's round; tiles left, that one included
-    int g;        // position in tile order, for the search of the tile's group
+    int r = 0;  // round of the next tile
+    int g = 0;  // position in tile order, for the search of the tile's group
 };
 
 template <int MODE, int TM, int TN>
@@ -334,7 +333,8 @@ struct Sched {
 
     __device__ __forceinline__ Tile decode(const Args& p, Walk& w) const {
         Tile T;
-        if (w.left <= 0) {
+        const int tile = tile_of(w.r);
+        if (tile >= total) {
             T.a = p.a;
             T.b = p.b;
             T.out = 0;
@@ -343,7 +343,6 @@ struct Sched {
             T.stages = 1;
             return T;
         }
-        const int tile = tile_of(w.r);
         while (tile_end[w.g] <= tile) ++w.g;
         w.g = (int)uni((uint32_t)w.g);
         const int first = w.g > 0 ? (int)uni((uint32_t)tile_end[w.g - 1]) : 0;
@@ -379,25 +378,6 @@ struct Sched {
     // longest first, in alternating directions, which evens out the sums.
     __device__ __forceinline__ int tile_of(int r) const {
         return r * nwg + (lpt && (r & 1) ? nwg - 1 - slot : slot);
-    }
-    // Where groups are the contraction (wgrad), each XCD begins an eighth of
-    // its rounds after the one before: at any time they are in groups of
-    // different lengths, and do not all write their tiles at once.
-    __device__ __forceinline__ Walk begin(int xcd) const {
-        Walk w;
-        const int full = total / nwg;
-        w.left = full + (tile_of(full) < total ? 1 : 0);
-        w.r = MODE == kWgrad ? w.left * xcd / 8 : 0;
-        w.g = 0;
-        return w;
-    }
-    __device__ __forceinline__ void next(Walk& w) const {
-        --w.left;
-        ++w.r;
-        if (MODE == kWgrad && tile_of(w.r) >= total) {
-            w.r = 0;
-            w.g = 0;
-        }
     }
 };
 
@@ -485,7 +465,6 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
     }
     S.total = (int)uni((uint32_t)table[G - 1]);
     if (S.slot >= S.total) return;
-    const Walk start = S.begin(bid % 8);
 
     const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
     Reader<TM, TA> ra;
@@ -501,14 +480,14 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
     // The loads run RING stages ahead of the products, over the ends of tiles:
     // they have a walk of their own.  A's go first; L is the tile they are in,
     // and B follows a step later.
-    Walk lw = start, cw = start;
+    Walk lw, cw;
     Tile L = S.decode(p, lw);
     uint32_t bcols = (uint32_t)L.cols;
     qa.start(L.a, (uint32_t)L.rows, L.k, lda2);
     qb.start(L.b, (uint32_t)L.cols, L.k, ldb2);
     auto advance_a = [&]() {
         if (!qa.advance((uint32_t)L.rows, lda2)) {
-            S.next(lw);
+            ++lw.r;
             L = S.decode(p, lw);
             qa.start(L.a, (uint32_t)L.rows, L.k, lda2);
         }
@@ -665,7 +644,7 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-        S.next(cw);
+        ++cw.r;
         C = S.decode(p, cw);
     }
     wait_loads<0>();
