@@ -152,6 +152,10 @@ mx_status mx_grad_norm(const void* plan, int32_t count, int64_t chunks, float ma
  *   scale = max(amax, 2^-100) / 448 over the block of 256, code = E4M3(x / scale)
  * with x = m, or x = sqrt(v), to nearest even; the code of a v > 0 is at
  * least the smallest one, 2^-9, so that no later step divides by eps alone.
+ * Every operation is rounded to fp32 by itself, in the order written here;
+ * x / scale is x times (1 / amax times 448), the scale amax times 1/448, the
+ * factors of the last line (1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 -
+ * beta2^t)) are formed in double.
  *   steps       int64 [2] on the device: [0] the number of steps done, which
  *               the call raises by one; [1] zero, used by the call
  *   lr, lr_device   the learning rate, or (not NULL) a float32 on the device
