@@ -31,6 +31,7 @@ hipError_t debug_take_quantize(uint32_t* out);
 hipError_t debug_take_dual(uint32_t* out);
 hipError_t debug_take_gemm(uint32_t* out);
 hipError_t debug_take_swiglu_quant(uint32_t* out);
+hipError_t debug_take_grouped_bf16(uint32_t* out);
 #endif
 }  // namespace mx
 
@@ -321,7 +322,8 @@ mx_status mx_debug_flags(uint32_t* flags, void* stream) {
     if (hipStreamSynchronize((hipStream_t)stream) != hipSuccess) return MX_ERR_HIP;
     uint32_t all = 0;
     for (hipError_t (*take)(uint32_t*) :
-         {mx::debug_take_quantize, mx::debug_take_dual, mx::debug_take_gemm, mx::debug_take_swiglu_quant}) {
+         {mx::debug_take_quantize, mx::debug_take_dual, mx::debug_take_gemm, mx::debug_take_swiglu_quant,
+          mx::debug_take_grouped_bf16}) {
         uint32_t w = 0;
         if (take(&w) != hipSuccess) return MX_ERR_HIP;
         all |= w;

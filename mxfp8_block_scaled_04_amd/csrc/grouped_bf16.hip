@@ -39,6 +39,7 @@
 // past K inside a row, whose offsets are moved out of range.
 #include <type_traits>
 
+#include "mx_debug.h"
 #include "mx_train.h"
 
 namespace mx {
@@ -423,6 +424,9 @@ __global__ __launch_bounds__((TM / WM) * (TN / WN) * 64, TM * RING >= 512 ? 1 : 
     S.tile_end = table;
     S.order = table + G;
     {
+        const int groups = G / p.split;
+        for (int g = t; g <= groups; g += kThreads)
+            debug_flag(offsets_entry_bad(p.offsets, g, groups, p.M), kDbgOffsets);
         int32_t* const order = table + G;
         if (S.lpt) {  // rank by length, longest first, ties by index
             for (int g = t; g < G; g += kThreads) table[g] = (int32_t)S.rows_of(p, g);
@@ -678,6 +682,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args p) {
     // threads.
     {
         if (t == 0) found[0] = -1;
+        for (int g = t; g <= p.G; g += WAVES * 64)
+            debug_flag(offsets_entry_bad(p.offsets, g, p.G, p.M), kDbgOffsets);
         const int per = (p.G + WAVES * 64 - 1) / (WAVES * 64);
         const auto rows_at = [&](int g, int64_t& lo) {
             lo = Sched<kForward, 256, 256>::bound(p, g);
@@ -861,6 +867,10 @@ __global__ __launch_bounds__(256) void join_kernel(const float* part, int64_t n,
 }
 
 }  // namespace
+
+#ifdef MXMOE_DEBUG
+hipError_t debug_take_grouped_bf16(uint32_t* out) { return debug_take_word(out); }
+#endif
 
 hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* offsets, int32_t G,
                                int64_t M, int64_t N, int64_t K, uint16_t* out, int64_t ldo, hipStream_t stream) {
