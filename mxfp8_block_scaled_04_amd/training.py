@@ -185,12 +185,14 @@ def mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K):
 
 class AdamWPlan:
     """A list of tensors as mx_grad_norm and mx_adamw take it: the device copy
-    of the plan and the workspace of the norm.  Keeps the tensors alive."""
+    of the plan and, behind it, the workspace of the norm.  Keeps the tensors
+    alive; to be kept itself until the calls that use it have run.  Calls of
+    mx_grad_norm on one plan share its workspace: on several streams, each
+    has to wait for the one before."""
 
-    def __init__(self, device, count, chunks, image, tensors):
+    def __init__(self, device, count, chunks, image, workspace_at, tensors):
         self.device, self.count, self.chunks, self.tensors = device, count, chunks, tensors
-        self.image = image
-        self.workspace = torch.zeros(int(_lib().mx_grad_norm_workspace_bytes()), dtype=torch.uint8, device=device)
+        self.image, self.workspace = image, image[workspace_at:]
         self.address, self.workspace_address = image.data_ptr(), self.workspace.data_ptr()
 
 
@@ -199,8 +201,9 @@ def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=
     lengths): weights and gradients float32 or bf16; states float32, or E4M3
     codes (uint8 or float8_e4m3fn) with float32 scales, one per 256 elements;
     masters float32, or None in the list or for all; weight_decay a number or
-    one per tensor.  Copies the plan to the GPU (synchronously): made once,
-    while the tensors stay where they are."""
+    one per tensor.  Copies the plan and the zeroed workspace of mx_grad_norm
+    to the GPU (synchronously: any stream can use them then): made once, while
+    the tensors stay where they are."""
     count = len(weights)
 
     def column(values, name):
@@ -239,12 +242,12 @@ def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=
         rows[i] = AdamwTensor(*address, n, float(decay[i]), (W_BF16 if w.dtype == torch.bfloat16 else 0)
                               | (G_BF16 if g.dtype == torch.bfloat16 else 0) | (STATE_8BIT if eight else 0))
     lib = _lib()
-    size = lib.mx_adamw_plan_bytes(rows, count)
-    image = torch.zeros(max(int(size), 16), dtype=torch.uint8)
+    at = max(16 * -(-int(lib.mx_adamw_plan_bytes(rows, count)) // 16), 0)  # (a list that is refused: below)
+    image = torch.zeros(at + int(lib.mx_grad_norm_workspace_bytes()), dtype=torch.uint8)
     chunks = ctypes.c_int64(0)
     _check(lib.mx_adamw_plan(rows, count, _ptr(image), ctypes.byref(chunks)), "mx_adamw_plan")
     device = weights[0].device if count else torch.device("cuda", torch.cuda.current_device())
-    return AdamWPlan(device, count, chunks.value, image.to(device),
+    return AdamWPlan(device, count, chunks.value, image.to(device), at,
                      [list(weights), grads, ms, vs, masters, m_scales, v_scales])
 
 
