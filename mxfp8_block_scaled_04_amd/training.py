@@ -100,6 +100,16 @@ def _same_device(first, *others):
         raise ValueError("all tensors must be on one GPU")
 
 
+def _empty(shape, dtype, device, stream):
+    """A buffer of a call's own, from the pool of the stream that writes it:
+    memory of another pool can still be in use on that pool's stream, and can
+    be given back there before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def mx_grouped_gemm_bf16(x, w, group_offsets, out=None, stream=None):
     """out[r] = x[r] w[g]^T for the rows r of group g: x bf16 [M, K] (row
     stride may exceed K), w bf16 [G, N, K], group_offsets int32 [G+1].
@@ -110,7 +120,7 @@ def mx_grouped_gemm_bf16(x, w, group_offsets, out=None, stream=None):
     if Kx != K:
         raise ValueError("K mismatch")
     if out is None:
-        out = torch.empty((M, N), dtype=_BF16, device=x.device)
+        out = _empty((M, N), _BF16, x.device, stream)
     Mo, No, ldo = _rows(out, "out")
     if Mo != M or No != N:
         raise ValueError("out shape")
@@ -130,7 +140,7 @@ def mx_grouped_gemm_bf16_dgrad(dy, w, group_offsets, dx=None, stream=None):
     if Ny != N:
         raise ValueError("N mismatch")
     if dx is None:
-        dx = torch.empty((M, K), dtype=_BF16, device=dy.device)
+        dx = _empty((M, K), _BF16, dy.device, stream)
     Mx, Kx, ldx = _rows(dx, "dx")
     if Mx != M or Kx != K:
         raise ValueError("dx shape")
@@ -155,7 +165,7 @@ def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, 
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw = torch.empty((G, N, K), dtype=_BF16, device=x.device)
+        dw = _empty((G, N, K), _BF16, x.device, stream)
     fp32 = dw.dtype is torch.float32
     if tuple(dw.shape) != (G, N, K) or not dw.is_contiguous() or not (fp32 or dw.dtype is _BF16):
         raise ValueError("dw must be a contiguous bf16 or float32 [G, N, K] tensor")
@@ -164,9 +174,8 @@ def mx_grouped_gemm_bf16_wgrad(dy, x, group_offsets, dw=None, accumulate=False, 
     size = 0
     if workspace is None:
         size = lib.mx_grouped_gemm_bf16_wgrad_workspace_bytes(G, M, N, K)
-        if size > 0:  # from the pool of the stream that uses it: it can be given back before the call has run
-            with torch.cuda.stream(stream):  # (None: the current one)
-                workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
+        if size > 0:
+            workspace = _empty(size, torch.uint8, dy.device, stream)
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     else:
@@ -256,7 +265,7 @@ def mx_grad_norm(plan, max_norm=float("inf"), out=None, stream=None):
     max_norm.  Returns out float32 [2]: the norm and the factor (NaN when the
     norm is not finite)."""
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=plan.device)
+        out = _empty(2, torch.float32, plan.device, stream)
     if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 [2] tensor")
     _same_device(plan.image, out)

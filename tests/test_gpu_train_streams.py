@@ -44,3 +44,25 @@ def test_norm_and_step_right_after_the_plan_was_made_on_a_busy_stream():
         assert all(torch.equal(a, b) for a, b in zip(tensors, first))
         assert not plan.workspace.view(torch.int64)[-1]  # the ticket, ready for the next call
         del keep
+
+
+def test_outputs_of_a_call_on_another_stream_are_not_memory_of_the_current_streams_pool():
+    off = torch.tensor([0, 400, 1000], dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(1)
+    x, w, dy = (torch.randn(s, generator=gen).bfloat16().cuda() for s in ((1000, 256), (2, 512, 256), (1000, 512)))
+    plan = mx.mx_adamw_plan(*([t] for t in _tensors()))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    calls = [lambda s: mx.mx_grouped_gemm_bf16(x, w, off, stream=s),
+             lambda s: mx.mx_grouped_gemm_bf16_dgrad(dy, w, off, stream=s),
+             lambda s: mx.mx_grouped_gemm_bf16_wgrad(dy, x, off, stream=s), lambda s: mx.mx_grad_norm(plan, stream=s)]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        freed = torch.empty_like(want)
+        at = freed.data_ptr()
+        del freed  # the block that the current stream's pool gives out next
+        got = call(side)
+        assert got.data_ptr() != at
+        side.synchronize()
+        assert torch.equal(got, want)

@@ -53,6 +53,18 @@ def _plan():
     return T.mx_adamw_plan(f, f, f, f)
 
 
+@pytest.mark.parametrize("side", [None, "another stream"])
+def test_buffers_of_a_call_come_from_the_pool_of_its_stream(made, side):
+    """Memory of another stream's pool can still be in use there."""
+    off = torch.tensor([0, 3], dtype=torch.int32)
+    T.mx_grouped_gemm_bf16(_bf16(3, 8), _bf16(1, 16, 8), off, stream=side)
+    T.mx_grouped_gemm_bf16_dgrad(_bf16(3, 16), _bf16(1, 16, 8), off, stream=side)
+    T.mx_grouped_gemm_bf16_wgrad(_bf16(3, 16), _bf16(3, 8), off, stream=side)
+    T.mx_grad_norm(_plan(), stream=side)
+    assert [m for m in made if m[0] != (0,)] == [((3, 16), side), ((3, 8), side), ((1, 16, 8), side), ((64,), side),
+                                                 ((2,), side)]
+
+
 def test_the_workspace_of_a_plan_is_zeroed_by_the_plans_own_copy(made, monkeypatch):
     """A fill on the stream that made the plan would not have run yet, or would
     run too late, for a norm on another stream."""
