@@ -76,7 +76,8 @@ int64_t mx_grouped_gemm_bf16_wgrad_workspace_bytes(int32_t G, int64_t M, int64_t
 enum {
     MX_ADAMW_W_BF16 = 1,     /* w is bf16 (else float32) */
     MX_ADAMW_G_BF16 = 2,     /* g is bf16 (else float32) */
-    MX_ADAMW_STATE_8BIT = 4  /* m and v are E4M3 codes with block scales (else float32) */
+    MX_ADAMW_STATE_8BIT = 4, /* m and v are E4M3 codes with block scales (else float32) */
+    MX_ADAMW_UNBIASED = 16   /* their codes are rounded at random, without bias (else to nearest) */
 };
 
 /* Elements per scale of an 8-bit state. */
@@ -94,6 +95,15 @@ enum {
  * An 8-bit state: block b holds elements [256 b, 256 b + 256).  m = m_scale[b]
  * code(m), v = (v_scale[b] code(v))^2, codes OCP E4M3FN (v: not negative).
  * Zero codes and scales are the state before the first step.
+ *
+ * Codes rounded to nearest hold their state for what a step changes by less
+ * than half a code's step: sqrt(v) falls by no more than 1 - sqrt(beta2) a
+ * step, so the code of an element that is not its block's largest stays for as
+ * long as the block's largest stays, whatever its own gradients do.  (Where one
+ * element of a block keeps its gradient and the others' fall to a hundredth,
+ * their v stays 10^4 times too large; with Gaussian gradients v is 15 % too
+ * large on average at beta2 = 0.95 and 24 % at 0.999.)  For training, set
+ * MX_ADAMW_UNBIASED: m and v are then right on average over the roundings.
  */
 typedef struct {
     void* w;
@@ -118,7 +128,7 @@ typedef struct {
  * MX_ERR_NULL: a required pointer is NULL (m_scale and v_scale are required
  * for 8-bit states); MX_ERR_SHAPE: count < 0, n < 0, unknown type bits, a
  * master with float32 weights, a weight decay that is negative or not
- * finite, scales with 32-bit states; MX_ERR_ALIGN: a pointer is not aligned
+ * finite, scales or unbiased codes with 32-bit states; MX_ERR_ALIGN: a pointer is not aligned
  * to its element; MX_ERR_UNSUPPORTED: more than 2^31 - 1 chunks.
  * mx_adamw_plan_bytes returns -1 for a list that mx_adamw_plan rejects for
  * its count or a length.
@@ -151,7 +161,13 @@ mx_status mx_grad_norm(const void* plan, int32_t count, int64_t chunks, float ma
  * The new w uses m and v before they are rounded to 8 bits:
  *   scale = max(amax, 2^-100) / 448 over the block of 256, code = E4M3(x / scale)
  * with x = m, or x = sqrt(v), to nearest even; the code of a v > 0 is at
- * least the smallest one, 2^-9, so that no later step divides by eps alone.
+ * least the smallest one, 2^-9, so that no later step divides by eps alone
+ * (below sqrt(v) = 2^-57 the code's square can underflow: there it does).
+ * Tensors with MX_ADAMW_UNBIASED take one of the two codes next to x / scale,
+ * at random: m's with the expected value x / scale, v's with the expected
+ * square (x / scale)^2 (up to that smallest code).  The random numbers depend
+ * on t and the element's index in its tensor only, so that the same step gives
+ * the same bits, in whatever list its tensor stands.
  * Every operation is rounded to fp32 by itself, in the order written here;
  * x / scale is x times (1 / amax times 448), the scale amax times 1/448, the
  * factors of the last line (1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 -

@@ -110,9 +110,10 @@ mx_status mx_adamw_plan(const mx_adamw_tensor* tensors, int32_t count, void* pla
         const mx_adamw_tensor& t = tensors[i];
         const bool wb = t.types & MX_ADAMW_W_BF16, gb = t.types & MX_ADAMW_G_BF16, s8 = t.types & MX_ADAMW_STATE_8BIT;
         if (t.n < 0 || t.n > INT64_MAX / 2) return MX_ERR_SHAPE;
-        if ((t.types & ~(uint32_t)(MX_ADAMW_W_BF16 | MX_ADAMW_G_BF16 | MX_ADAMW_STATE_8BIT)) != 0) return MX_ERR_SHAPE;
+        if ((t.types & ~(uint32_t)(MX_ADAMW_W_BF16 | MX_ADAMW_G_BF16 | MX_ADAMW_STATE_8BIT | MX_ADAMW_UNBIASED)) != 0)
+            return MX_ERR_SHAPE;
         if ((t.master && !wb) || !(t.weight_decay >= 0.0f) || !std::isfinite(t.weight_decay)) return MX_ERR_SHAPE;
-        if (!s8 && (t.m_scale || t.v_scale)) return MX_ERR_SHAPE;
+        if (!s8 && (t.m_scale || t.v_scale || (t.types & MX_ADAMW_UNBIASED))) return MX_ERR_SHAPE;
         if (t.n == 0) continue;
         if (!t.w || !t.g || !t.m || !t.v || (s8 && (!t.m_scale || !t.v_scale))) return MX_ERR_NULL;
         const size_t state = s8 ? 1 : 4;

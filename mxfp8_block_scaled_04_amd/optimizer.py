@@ -12,7 +12,8 @@ class AdamW:
     grads: the tensors (float32 or bf16, same lengths) that hold their
     gradients at every step.  bf16 weights get float32 masters unless
     masters=False.  state_bits: 32, or 8 (E4M3 codes of m and sqrt(v) with a
-    float32 scale per 256 elements).  weight_decay: a number or one per
+    float32 scale per 256 elements, rounded at random without bias; the same
+    step gives the same bits).  weight_decay: a number or one per
     tensor.  max_norm: clip by the gradients' global norm; a step whose norm
     is infinite or NaN then changes nothing."""
 
@@ -40,7 +41,8 @@ class AdamW:
             (zeros(torch.float32, lambda w: -(-w.numel() // BLOCK)) for _ in range(2)) if state_bits == 8
             else (None, None))
         self.plan = mx_adamw_plan(self.weights, self.grads, self.m, self.v, masters=self.masters,
-                                  m_scales=self.m_scale, v_scales=self.v_scale, weight_decay=weight_decay)
+                                  m_scales=self.m_scale, v_scales=self.v_scale, weight_decay=weight_decay,
+                                  unbiased=state_bits == 8)
 
     def set_lr(self, lr):
         self.lr.fill_(lr)

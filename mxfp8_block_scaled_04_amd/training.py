@@ -14,7 +14,7 @@ from . import _check, _ptr, load
 
 BLOCK = 256  # elements per scale of an 8-bit optimizer state
 
-W_BF16, G_BF16, STATE_8BIT = 1, 2, 4
+W_BF16, G_BF16, STATE_8BIT, UNBIASED = 1, 2, 4, 16
 
 # Exported C symbols of include/libmxmoe_train.h, in its order.
 TRAIN_SYMBOLS = (
@@ -205,12 +205,16 @@ class AdamWPlan:
         self.address, self.workspace_address = image.data_ptr(), self.workspace.data_ptr()
 
 
-def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=None, weight_decay=0.0):
+def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=None, weight_decay=0.0,
+                  unbiased=False):
     """Plan of the tensors (lists of contiguous GPU tensors of the same
     lengths): weights and gradients float32 or bf16; states float32, or E4M3
     codes (uint8 or float8_e4m3fn) with float32 scales, one per 256 elements;
     masters float32, or None in the list or for all; weight_decay a number or
-    one per tensor.  Copies the plan and the zeroed workspace of mx_grad_norm
+    one per tensor.  unbiased: 8-bit states are rounded at random, so that they
+    are right on average (to be set for training: to nearest, which is the
+    default of mx_adamw_tensor, a slowly falling v stays where it is; see
+    include/libmxmoe_train.h).  Copies the plan and the zeroed workspace of mx_grad_norm
     to the GPU (synchronously: any stream can use them then): made once, while
     the tensors stay where they are."""
     count = len(weights)
@@ -249,7 +253,8 @@ def mx_adamw_plan(weights, grads, ms, vs, masters=None, m_scales=None, v_scales=
         _same_device(weights[0], *given)
         address = [None if t is None or t.numel() == 0 else t.data_ptr() for t in (w, master, g, m, v, msc, vsc)]
         rows[i] = AdamwTensor(*address, n, float(decay[i]), (W_BF16 if w.dtype == torch.bfloat16 else 0)
-                              | (G_BF16 if g.dtype == torch.bfloat16 else 0) | (STATE_8BIT if eight else 0))
+                              | (G_BF16 if g.dtype == torch.bfloat16 else 0) | (STATE_8BIT if eight else 0)
+                              | (UNBIASED if eight and unbiased else 0))
     lib = _lib()
     at = max(16 * -(-int(lib.mx_adamw_plan_bytes(rows, count)) // 16), 0)  # (a list that is refused: below)
     image = torch.zeros(at + int(lib.mx_grad_norm_workspace_bytes()), dtype=torch.uint8)
