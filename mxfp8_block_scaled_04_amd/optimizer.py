@@ -26,6 +26,8 @@ class AdamW:
         self.weights, self.grads = list(weights), list(grads)
         self.beta1, self.beta2 = betas
         self.eps, self.max_norm = eps, max_norm
+        self.weight_decay = ([float(weight_decay)] * len(self.weights) if isinstance(weight_decay, (int, float))
+                             else [float(d) for d in weight_decay])
         device = self.weights[0].device
         self.lr = torch.tensor([lr], dtype=torch.float32, device=device)
         self.steps = torch.zeros(2, dtype=torch.int64, device=device)
@@ -41,7 +43,7 @@ class AdamW:
             (zeros(torch.float32, lambda w: -(-w.numel() // BLOCK)) for _ in range(2)) if state_bits == 8
             else (None, None))
         self.plan = mx_adamw_plan(self.weights, self.grads, self.m, self.v, masters=self.masters,
-                                  m_scales=self.m_scale, v_scales=self.v_scale, weight_decay=weight_decay,
+                                  m_scales=self.m_scale, v_scales=self.v_scale, weight_decay=self.weight_decay,
                                   unbiased=state_bits == 8)
 
     def set_lr(self, lr):
@@ -60,15 +62,29 @@ class AdamW:
         out = {f"{k}.{i}": t for k, ts in lists.items() for i, t in enumerate(ts) if t is not None}
         return {**out, "steps": self.steps, "lr": self.lr}
 
+    def _settings(self):
+        """What the constructor was given and a step depends on."""
+        values = {"betas": [self.beta1, self.beta2], "eps": [self.eps], "weight_decay": self.weight_decay,
+                  "max_norm": [-1.0 if self.max_norm is None else self.max_norm]}  # (-1: no clipping)
+        return {k: torch.tensor(v, dtype=torch.float64) for k, v in values.items()}
+
     def state_dict(self):
-        """Copies of everything that a later step depends on (weights too)."""
-        return {k: t.clone() for k, t in self._tensors().items()}
+        """Copies of everything that a later step depends on (weights and
+        settings too)."""
+        return {**{k: t.clone() for k, t in self._tensors().items()}, **self._settings()}
 
     def load_state_dict(self, state):
-        """Into the tensors that are there: the plan stays valid."""
-        mine = self._tensors()
-        if set(state) != set(mine) or any(state[k].shape != t.shape or state[k].dtype != t.dtype
-                                          for k, t in mine.items()):
+        """Into the tensors that are there: the plan stays valid.  The learning
+        rate is loaded; other settings (betas, eps, weight decay, max_norm) are
+        part of the plan and of captured steps, and have to be those of this
+        optimizer (a state that has none of them is taken as it is)."""
+        mine, settings = self._tensors(), self._settings()
+        wanted = set(mine) | (set(settings) if set(settings) & set(state) else set())
+        if set(state) != wanted or any(state[k].shape != t.shape or state[k].dtype != t.dtype
+                                       for k, t in mine.items()):
             raise ValueError("the state is not of these tensors")
+        for k, t in settings.items():
+            if k in state and not torch.equal(state[k].double().cpu(), t):
+                raise ValueError(f"{k}: the state was saved with {state[k].tolist()}, this optimizer has {t.tolist()}")
         for k, t in mine.items():
             t.copy_(state[k])
