@@ -8,14 +8,14 @@ from .training import BLOCK, mx_adamw, mx_adamw_plan, mx_grad_norm
 
 
 class AdamW:
-    """weights: float32 or bf16 GPU tensors, updated in place by step();
-    grads: the tensors (float32 or bf16, same lengths) that hold their
-    gradients at every step.  bf16 weights get float32 masters unless
+    """weights: float32 or bf16 GPU tensors (parameters too), updated in place
+    by step(); grads: the tensors (float32 or bf16, same lengths) that hold
+    their gradients at every step.  bf16 weights get float32 masters unless
     masters=False.  state_bits: 32, or 8 (E4M3 codes of m and sqrt(v) with a
     float32 scale per 256 elements, rounded at random without bias; the same
-    step gives the same bits).  weight_decay: a number or one per
-    tensor.  max_norm: clip by the gradients' global norm; a step whose norm
-    is infinite or NaN then changes nothing."""
+    step gives the same bits).  weight_decay: a number or one per tensor.
+    max_norm: clip by the gradients' global norm; a step whose norm is
+    infinite or NaN then changes nothing."""
 
     def __init__(self, weights, grads, lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, state_bits=32,
                  masters=True, max_norm=None):
@@ -23,7 +23,8 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32")
         if not weights:
             raise ValueError("no tensors")
-        self.weights, self.grads = list(weights), list(grads)
+        # (without autograd: the same memory, which step() writes through the plan)
+        self.weights, self.grads = [w.detach() for w in weights], [g.detach() for g in grads]
         self.beta1, self.beta2 = betas
         self.eps, self.max_norm = eps, max_norm
         self.weight_decay = ([float(weight_decay)] * len(self.weights) if isinstance(weight_decay, (int, float))

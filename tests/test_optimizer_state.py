@@ -17,6 +17,21 @@ def _make(weights=None, **kwargs):
     return AdamW(weights, [torch.zeros(300), torch.zeros(4)], **{"lr": 1e-2, "weight_decay": [0.1, 0.0], **kwargs})
 
 
+def test_parameters_are_updated_outside_of_autograd():
+    """Weights that require gradients: their masters, checkpoints and loading
+    belong to no graph, and the parameter keeps its memory."""
+    p, q = (torch.nn.Parameter(torch.ones(n, dtype=d)) for n, d in ((300, torch.float32), (4, torch.bfloat16)))
+    opt = _make([p, q])
+    assert opt.weights[0].data_ptr() == p.data_ptr() and not opt.masters[1].requires_grad
+    saved = opt.state_dict()
+    assert not any(t.requires_grad for t in saved.values())
+    saved["weights.0"].fill_(5.0)
+    saved["masters.1"].fill_(6.0)
+    opt.load_state_dict(saved)
+    assert (p == 5).all() and (opt.masters[1] == 6).all()
+    assert p.requires_grad and p.is_leaf and q.requires_grad and q.is_leaf
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("name,value", [("betas", (0.9, 0.999)), ("betas", (0.8, 0.95)), ("eps", 1e-6),
                                         ("max_norm", 1.0), ("max_norm", float("inf")), ("weight_decay", 0.1),
