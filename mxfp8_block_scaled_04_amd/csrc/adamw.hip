@@ -508,8 +508,8 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const AdamwEntry* e
         const double norm = sqrt(all);
         const float rounded = (float)norm;
         out[0] = rounded;
-        out[1] = rounded <= __FLT_MAX__ ? fminf(1.0f / rounded * max_norm, 1.0f)
-                                        : __builtin_nanf("");
+        // (one division: the reciprocal of a norm below 2^-128 is infinite)
+        out[1] = rounded <= __FLT_MAX__ ? fminf(max_norm / rounded, 1.0f) : __builtin_nanf("");
         __hip_atomic_store(&ws->ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
