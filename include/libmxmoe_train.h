@@ -157,7 +157,9 @@ mx_status mx_grad_norm(const void* plan, int32_t count, int64_t chunks, float ma
  *   g' = c g
  *   m  = beta1 m + (1 - beta1) g'
  *   v  = beta2 v + (1 - beta2) g'^2
- *   w  = (1 - lr decay) w - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   w  = keep w - size (m / (sqrt(v) root + eps))
+ * with keep = 1 - lr decay, size = lr / (1 - beta1^t), root = 1 / sqrt(1 -
+ * beta2^t), each formed in double and rounded to fp32 once.
  * The new w uses m and v before they are rounded to 8 bits:
  *   scale = max(amax, 2^-100) / 448 over the block of 256, code = E4M3(x / scale)
  * with x = m, or x = sqrt(v), to nearest even; the code of a v > 0 is at
@@ -165,17 +167,17 @@ mx_status mx_grad_norm(const void* plan, int32_t count, int64_t chunks, float ma
  * (below sqrt(v) = 2^-57 the code's square can underflow: there it does).
  * Tensors with MX_ADAMW_UNBIASED take one of the two codes next to x / scale,
  * at random: m's with the expected value x / scale, v's with the expected
- * square (x / scale)^2 (up to that smallest code).  The random numbers depend
+ * square (x / scale)^2 (but for that smallest code).  The random numbers depend
  * on t and the element's index in its tensor only, so that the same step gives
  * the same bits, in whatever list its tensor stands.
- * Every operation is rounded to fp32 by itself, in the order written here;
- * x / scale is x times (1 / amax times 448), the scale amax times 1/448, the
- * factors of the last line (1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 -
- * beta2^t)) are formed in double.
+ * Every operation is rounded to fp32 by itself, in the order that the
+ * parentheses give; x / scale is x times ((1 / amax) times 448), the scale amax
+ * times 1/448.
  *   steps       int64 [2] on the device: [0] the number of steps done, which
  *               the call raises by one; [1] zero, used by the call
  *   lr, lr_device   the learning rate, or (not NULL) a float32 on the device
  *               to take in its place, for captured graphs with a schedule
+ *               (taken as it is: one that is not finite reaches the weights)
  *   grad_scale  float32 on the device or NULL.  If it is negative or not
  *               finite, the call changes nothing (out + 1 of mx_grad_norm:
  *               a step with infinite or NaN gradients is left out)

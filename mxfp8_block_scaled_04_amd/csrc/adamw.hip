@@ -4,7 +4,8 @@
 // Mathematics (fp32, per element; t = step count after this step, c = the
 // gradients' factor):
 //   g' = c g,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
-//   w  = (1 - lr d) w - [lr / (1 - b1^t)] m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//   w  = [1 - lr d] w - [lr / (1 - b1^t)] (m / (sqrt(v) [1 / sqrt(1 - b2^t)] + eps))
+// (the factors in brackets once a step, in double).
 // 8-bit states hold m and sqrt(v) as E4M3 codes under one fp32 scale per 256
 // elements, scale = max(amax, 2^-100) / 448.  sqrt(v) and not v: E4M3 spans
 // 2^17.8 from its smallest code to 448, which is 2^35 in v.  The scale is a
