@@ -184,8 +184,9 @@ mx_status mx_grad_norm(const void* plan, int32_t count, int64_t chunks, float ma
  * Without such a factor a NaN or infinity in g reaches m, v and w of its
  * element and, with 8-bit states, the states of its block.
  * MX_ERR_SHAPE unless 0 <= beta1 < 1, 0 <= beta2 < 1, eps >= 0 and lr are
- * finite and count and chunks not negative.  count, chunks: the plan's; an
- * empty plan still counts the step.
+ * finite and count and chunks not negative (with eps = 0 a weight whose v is
+ * 0 becomes NaN, as the formula has it).  count, chunks: the plan's; an empty
+ * plan still counts the step.
  */
 mx_status mx_adamw(const void* plan, int32_t count, int64_t chunks, int64_t* steps, double lr, const float* lr_device,
                    double beta1, double beta2, double eps, const float* grad_scale, void* stream);

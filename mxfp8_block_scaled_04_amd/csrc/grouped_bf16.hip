@@ -12,9 +12,13 @@
 //
 // What bounds it: with many rows a group the operand loads and the matrix
 // pipes, at the clock that the power limit leaves (forward, 32768 x 4096 x
-// 7168, 16 groups: 1.65 ms, 1.17 PFLOP/s, pipes busy 68 %; dgrad, 7168 x 2048:
-// 0.89 ms; wgrad of the same, added to fp32 values: 1.11 ms, of which the
-// values are 1.9 GB); with few rows reading the weights (few_rows_kernel).
+// 7168, 16 groups: 1.65-1.67 ms, 1.16 PFLOP/s, pipes busy 68 %; dgrad, 7168 x
+// 2048: 0.89 ms, of which 15 % are a last round of tiles for a quarter of the
+// CUs; wgrad of the same to bf16 0.84 ms, to fp32 0.95 ms, added to fp32 values
+// 1.13 ms, of which the values are 1.9 GB); with few rows reading the weights
+// (few_rows_kernel); with thousands of groups finding the tiles' groups (256 x
+// 256 weights, 16 rows a group: 128 groups 19 us, 1024 groups 109 us, 4096
+// groups 856 us).
 //
 // Layout: persistent workgroups of 4 waves, one 256 x 256 tile per CU (128 x
 // 128 per wave) or two 128 x 128 tiles per CU (64 x 64 per wave),
@@ -22,10 +26,10 @@
 // operands (64 KB for the large tile), loaded straight into LDS by 16-byte
 // direct loads; two stages in LDS (four for small tiles that have a CU to
 // themselves).  A stage has 4 steps of 16: the fragments of a step are read
-// while the one before is multiplied, also across stages and tiles.  The wait for the next stage and the barrier sit before a
-// stage's last step, whose fragments are in registers by then; the loads of
-// the stage after the next go into the buffer freed by that barrier, spread
-// over two steps.
+// while the one before is multiplied, also across stages and tiles.  The wait
+// for the next stage and the barrier sit before a stage's last step, whose
+// fragments are in registers by then; the loads of the stage after the next go
+// into the buffer freed by that barrier, spread over two steps.
 // Tried and slower at 32768 x 4096 x 7168 (16 groups, 1.63 ms as it is, 1.18
 // ms without its loads): 8 waves of 128 x 64 (1.73 ms: a third more LDS
 // reads), the same in two groups of opposite phase (1.72 ms), stages of 32
@@ -224,12 +228,11 @@ struct Loader {
     __device__ __forceinline__ void begin(int slot) {
         lds = uni(lds0 + (uint32_t)slot * (ROWS * SK * 2));
     }
-    // instruction j of the wave
-    // instruction J of the wave
     template <int J>
     __device__ __forceinline__ void load() {
         load_to_lds<J * 1024>(d, voff[kind(J)], soff[J], lds);
     }
+    // instruction j of the wave
     __device__ __forceinline__ void load(int j) {
         if (j == 0) load<0>();
         if (j == 1) load<1>();
@@ -383,7 +386,8 @@ struct Sched {
 };
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
-    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)y) << 16);
+    const uint32_t lo = __builtin_bit_cast(uint16_t, (__bf16)x), hi = __builtin_bit_cast(uint16_t, (__bf16)y);
+    return lo | (hi << 16);
 }
 
 // Keeps the accumulators of row blocks i and on where the matrix instructions
@@ -802,10 +806,13 @@ int64_t tile_bound(const Args& p, int64_t tm, int64_t tn) {
 }
 
 // Whether a forward product goes to few_rows_kernel: on average at most 8 rows
-// a group (at 8, 128 rows of 16 groups at 4096 x 7168, both kernels take 198
-// us; at 4 it has 99 against 121 us, at 16 278 against 199), or few rows at
-// all (tiles would leave most CUs idle).  K: 16 rows of weights are a
-// descriptor's range.
+// a group (16 groups, 4096 x 7168: 64 rows 99 against 121 us in tiles, 128 rows
+// 198 us in both, 256 rows 278 against 199; 1024 rows of 128 groups are past the
+// break-even, 1520 against 1218 us), or few rows at all, where tiles leave most
+// CUs idle (one group, 4096 x 7168: 16 rows 17 against 49 us, 32 rows 28 against
+// 49, 64 rows 53 against 49; at 1024 x 1024, 64 rows, 11 against 13).  The host
+// knows the average only: each 16 rows of a group read its weights again, so
+// that 1000 rows which all fall to one of 128 groups take 798 us (108 in tiles).
 bool few_rows(const Args& p) { return p.M <= 8 * (int64_t)p.G || p.M <= 64; }
 
 template <int MODE, int OUT>
@@ -893,7 +900,8 @@ hipError_t launch_grouped_bf16_dgrad(const uint16_t* dy, int64_t ldy, const uint
 
 // Slices of each group's rows: where small tiles leave workgroup slots empty
 // and the groups are long, so that a slice has 1024 rows or more on average
-// (65536 rows, 8 groups, 512 x 512: 8 slices 109 us, none 260 us).
+// (65536 rows, 8 groups, 512 x 512, 4 slices each: 52 us, 62 us without; where
+// one group has 45 % of the rows, whose slices are the longest, 109 and 195 us).
 int32_t wgrad_split(int32_t G, int64_t M, int64_t N, int64_t K) {
     const int64_t small = (int64_t)G * tiles(N, 128) * tiles(K, 128), slots = 512;
     int64_t s = small > 0 ? slots / small : 1;

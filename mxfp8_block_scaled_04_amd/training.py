@@ -19,7 +19,8 @@ W_BF16, G_BF16, STATE_8BIT, UNBIASED = 1, 2, 4, 16
 # Exported C symbols of include/libmxmoe_train.h, in its order.
 TRAIN_SYMBOLS = (
     "mx_grouped_gemm_bf16", "mx_grouped_gemm_bf16_dgrad", "mx_grouped_gemm_bf16_wgrad",
-    "mx_grouped_gemm_bf16_wgrad_workspace_bytes", "mx_adamw_plan_bytes", "mx_adamw_plan", "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw",
+    "mx_grouped_gemm_bf16_wgrad_workspace_bytes", "mx_adamw_plan_bytes", "mx_adamw_plan",
+    "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw",
 )
 
 
