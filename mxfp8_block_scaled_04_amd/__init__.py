@@ -463,3 +463,8 @@ def mx_grouped_gemm_wgrad(A, As, B, Bs, padded_offsets, dW=None, stream=None):
 from .training import (  # noqa: E402
     TRAIN_SYMBOLS, AdamWPlan, mx_adamw, mx_adamw_plan, mx_grad_norm, mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad,
     mx_grouped_gemm_bf16_wgrad, mx_grouped_gemm_bf16_wgrad_workspace_bytes)
+
+# What surrounds the experts (include/libmxmoe_block.h).
+from .block import (  # noqa: E402
+    BLOCK_SYMBOLS, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward, mx_rms_norm_backward_workspace_bytes,
+    mx_router, mx_router_backward)

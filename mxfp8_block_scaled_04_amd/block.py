@@ -1,0 +1,272 @@
+"""Python binding of what surrounds the experts: the router and its gradient,
+the gradient of the routing weights through the combine, and the
+root-mean-square norm with its gradient (see include/libmxmoe_block.h for the
+contract of each call).
+
+Argument marshalling only, as in the package's main module, which re-exports
+everything here: every step runs in the HIP kernels, and there is no
+fallback.  A call runs on the GPU of its tensors, on that GPU's current stream
+unless it is given one.
+"""
+import ctypes
+
+import torch
+
+from . import _check, load, mx_scale_bytes
+from .training import _empty, _same_device
+
+SIGMOID, RENORM, LOGITS_BF16 = 1, 2, 4
+STREAM_FP32, WEIGHT_FP32 = 1, 2
+
+# Exported C symbols of include/libmxmoe_block.h, in its order.
+BLOCK_SYMBOLS = (
+    "mx_router", "mx_router_backward", "mx_combine_dweights", "mx_rms_norm", "mx_rms_norm_backward",
+    "mx_rms_norm_backward_workspace_bytes",
+)
+
+_BF16, _FP32, _INT32, _UINT8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+_signed = None
+
+
+def _lib():
+    """The library, with the signatures of this module's calls set."""
+    global _signed
+    lib = load()  # (another one if a program opens a build of its own)
+    if _signed is not lib:
+        P, I64, I32, U32, F, ST = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float,
+                                   ctypes.c_int)
+        for name, args, result in (
+            ("mx_router", [P, I64, I64, I32, P, I32, I32, I32, I32, F, U32, P, P, P, P], ST),
+            ("mx_router_backward", [P, I64, I64, I32, P, P, P, I32, F, U32, P, I64, P], ST),
+            ("mx_combine_dweights", [P, I64, P, I64, I64, P, I64, I32, I64, P, P], ST),
+            ("mx_rms_norm", [P, I64, P, I64, P, I64, I64, F, U32, P, I64, P, I64, P, P, P, P], ST),
+            ("mx_rms_norm_backward", [P, I64, P, I64, P, I64, P, P, P, I64, I64, I64, U32, P, I64, P, I64, P, I32, I32,
+                                      P, I64, P], ST),
+            ("mx_rms_norm_backward_workspace_bytes", [I64, I64], I64),
+        ):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, result
+        _signed = lib
+    return lib
+
+
+def _call(name, at, stream, *args):
+    """The call on GPU `at`, which need not be the current one."""
+    if stream is None:
+        handle = torch.cuda.current_stream(at).cuda_stream
+    elif stream.device.index != at:
+        raise ValueError("the stream is of another GPU than the tensors")
+    else:
+        handle = stream.cuda_stream
+    f = getattr(_lib(), name)
+    if at == torch.cuda.current_device():
+        rc = f(*args, handle)
+    else:
+        with torch.cuda.device(at):
+            rc = f(*args, handle)
+    _check(rc, name)
+
+
+def _matrix(t, name, dtypes, shape=None):
+    """The row stride of a matrix whose rows are contiguous."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, not {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a matrix" + ("" if shape is None else f" of {shape[0]} x {shape[1]}"))
+    rows, columns = t.shape
+    if columns > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return 8 * -(-columns // 8) if rows <= 1 or columns == 0 else t.stride(0)  # (not used)
+
+
+def _whole(t, name, dtypes, shape):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, not {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {' x '.join(map(str, shape))}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _flags(score, renorm, logits):
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return (SIGMOID if score == "sigmoid" else 0) | (RENORM if renorm else 0) | (
+        LOGITS_BF16 if logits.dtype is _BF16 else 0)
+
+
+def mx_router(logits, k, bias=None, groups=1, groups_kept=None, group_top=2, score="softmax", renorm=True, scale=1.0,
+              experts=None, weights=None, scores=None, stream=None):
+    """logits float32 or bf16 [T, E] (row stride may exceed E) -> (experts int32
+    [T, k], weights float32 [T, k], scores float32 [T, E] or None): the k
+    experts of the largest score (+ bias float32 [E]) of each token, largest
+    first, and their weights, as mx_route_plan and mx_combine take them (-1 and
+    0 where a mask of -infinity leaves fewer).  score: "softmax" or "sigmoid";
+    groups, groups_kept (default: all), group_top: choose among the experts of
+    the groups_kept groups of the largest sums of group_top choices; renorm:
+    weights are divided by their sum; scale: their factor.  scores: None, True
+    (allocate) or a tensor that receives all scores."""
+    ldl = _matrix(logits, "logits", (_FP32, _BF16))
+    T, E = logits.shape
+    flags = _flags(score, renorm, logits)
+    if experts is None:
+        experts = _empty((T, k), _INT32, logits.device, stream)
+    if weights is None:
+        weights = _empty((T, k), _FP32, logits.device, stream)
+    if scores is True:
+        scores = _empty((T, E), _FP32, logits.device, stream)
+    _whole(experts, "experts", (_INT32,), (T, k))
+    _whole(weights, "weights", (_FP32,), (T, k))
+    if scores is not None:
+        _whole(scores, "scores", (_FP32,), (T, E))
+    if bias is not None:
+        _whole(bias, "bias", (_FP32,), (E,))
+    _same_device(logits, bias, experts, weights, scores)
+    _call("mx_router", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, _at(bias), groups,
+          groups if groups_kept is None else groups_kept, group_top, k, scale, flags, experts.data_ptr(),
+          weights.data_ptr(), _at(scores))
+    return experts, weights, scores
+
+
+def mx_router_backward(logits, experts, dweights, dscores=None, score="softmax", renorm=True, scale=1.0, dlogits=None,
+                       stream=None):
+    """Gradient of the logits [T, E] from that of the weights (dweights float32
+    [T, k], of the experts int32 [T, k] that mx_router chose with the same
+    score, renorm and scale) and, if given, of all scores (dscores float32
+    [T, E]).  Returns dlogits of the logits' type."""
+    ldl = _matrix(logits, "logits", (_FP32, _BF16))
+    T, E = logits.shape
+    k = experts.shape[1] if experts.dim() == 2 else 0
+    _whole(experts, "experts", (_INT32,), (T, k))
+    _whole(dweights, "dweights", (_FP32,), (T, k))
+    if dscores is not None:
+        _whole(dscores, "dscores", (_FP32,), (T, E))
+    flags = _flags(score, renorm, logits)
+    if dlogits is None:
+        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
+    ldd = _matrix(dlogits, "dlogits", (logits.dtype,), (T, E))
+    _same_device(logits, experts, dweights, dscores, dlogits)
+    _call("mx_router_backward", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, experts.data_ptr(),
+          dweights.data_ptr(), _at(dscores), k, scale, flags, dlogits.data_ptr(), ldd)
+    return dlogits
+
+
+def mx_combine_dweights(dout, y, slot_of, dweights=None, stream=None):
+    """Gradient of mx_combine's weights: dout bf16 [T, N], y bf16 [M, N]
+    expert-ordered rows, slot_of int32 [T, k] -> float32 [T, k], the products
+    of each token's output gradient with its expert rows (0 where it has none)."""
+    ldd = _matrix(dout, "dout", (_BF16,))
+    T, N = dout.shape
+    ldy = _matrix(y, "y", (_BF16,), (y.shape[0], N))
+    k = slot_of.shape[1] if slot_of.dim() == 2 else 0
+    _whole(slot_of, "slot_of", (_INT32,), (T, k))
+    if dweights is None:
+        dweights = _empty((T, k), _FP32, dout.device, stream)
+    _whole(dweights, "dweights", (_FP32,), (T, k))
+    _same_device(dout, y, slot_of, dweights)
+    _call("mx_combine_dweights", dout.get_device(), stream, dout.data_ptr(), ldd, y.data_ptr(), y.shape[0], ldy,
+          slot_of.data_ptr(), T, k, N, dweights.data_ptr())
+    return dweights
+
+
+def mx_rms_norm(x, weight, residual=None, eps=1e-6, h=None, y=True, q=None, s=None, rstd=None, stream=None):
+    """Root-mean-square norm of the rows of x + residual, and its MXFP8 rows.
+    x bf16 [M, N]; residual None or bf16 or float32 [M, N] (without one x may
+    be float32); weight bf16 or float32 [N].  y, q, s, rstd: None (not
+    written), True (allocated) or a tensor: y bf16 [M, N], q uint8 [M, N] codes
+    and s their packed scales (with q; as mx_quantize_rows of y writes them),
+    rstd float32 [M] for the backward pass.  h: the sum, allocated with a
+    residual if None; it may be the residual itself.  Returns (y, h, q, s, rstd);
+    h is None without a residual."""
+    if residual is None:
+        ldx, ldr, kind = _matrix(x, "x", (_BF16, _FP32)), 0, x.dtype
+        if h is not None:
+            raise ValueError("h is written with a residual only")
+    else:
+        ldx, ldr = _matrix(x, "x", (_BF16,)), _matrix(residual, "residual", (_BF16, _FP32), tuple(x.shape))
+        kind = residual.dtype
+    M, N = x.shape
+    dev = x.device
+    _whole(weight, "weight", (_BF16, _FP32), (N,))
+    if residual is not None and h is None:
+        h = _empty((M, N), kind, dev, stream)
+    if y is True:
+        y = _empty((M, N), _BF16, dev, stream)
+    if q is None and s is not None:
+        raise ValueError("s is written with q only")
+    if q is True:
+        q = _empty((M, N), _UINT8, dev, stream)
+    if q is not None and (s is None or s is True):
+        s = _empty((mx_scale_bytes(M, N),), _UINT8, dev, stream)
+    if rstd is True:
+        rstd = _empty((M,), _FP32, dev, stream)
+    ldh = 0 if h is None else _matrix(h, "h", (kind,), (M, N))
+    ldy = 0 if y is None else _matrix(y, "y", (_BF16,), (M, N))
+    if q is not None:
+        _whole(q, "q", (_UINT8,), (M, N))
+        _whole(s, "s", (_UINT8,), (mx_scale_bytes(M, N),))
+    if rstd is not None:
+        _whole(rstd, "rstd", (_FP32,), (M,))
+    _same_device(x, residual, weight, h, y, q, s, rstd)
+    flags = (STREAM_FP32 if kind is _FP32 else 0) | (WEIGHT_FP32 if weight.dtype is _FP32 else 0)
+    _call("mx_rms_norm", x.get_device(), stream, x.data_ptr(), ldx, _at(residual), ldr, weight.data_ptr(), M, N, eps,
+          flags, _at(h), ldh, _at(y), ldy, _at(q), _at(s), _at(rstd))
+    return y, h, q, s, rstd
+
+
+def mx_rms_norm_backward(dy, h, weight, rstd, dy2=None, dh_in=None, dh=None, dx=None, dweight=True, accumulate=False,
+                         workspace=None, stream=None):
+    """Gradients of mx_rms_norm: dy (and dy2) bf16 [M, N] gradients of y, h and
+    rstd of the forward pass (h = x without a residual), dh_in the gradient
+    that reaches h from behind, of h's type.  Returns (dh, dx, dweight): dh of
+    h's type, the gradient of x and of the residual; dx None, or its bf16
+    rounding where h is float32 (True: allocated); dweight [N]: None (left
+    out), True (allocated in the weight's type), a dtype, or a bf16 or float32
+    tensor, which accumulate adds to (float32).  workspace: a uint8 tensor of
+    mx_rms_norm_backward_workspace_bytes, allocated on the stream's behalf if
+    None."""
+    ldh = _matrix(h, "h", (_BF16, _FP32))
+    M, N = h.shape
+    kind, dev = h.dtype, h.device
+    ldy = _matrix(dy, "dy", (_BF16,), (M, N))
+    ldy2 = 0 if dy2 is None else _matrix(dy2, "dy2", (_BF16,), (M, N))
+    ldi = 0 if dh_in is None else _matrix(dh_in, "dh_in", (kind,), (M, N))
+    _whole(weight, "weight", (_BF16, _FP32), (N,))
+    _whole(rstd, "rstd", (_FP32,), (M,))
+    if dh is None:
+        dh = _empty((M, N), kind, dev, stream)
+    if dx is True:
+        dx = _empty((M, N), _BF16, dev, stream)
+    if accumulate and not isinstance(dweight, torch.Tensor):
+        raise ValueError("accumulate needs dweight")
+    if dweight is True or isinstance(dweight, torch.dtype):
+        dweight = _empty((N,), weight.dtype if dweight is True else dweight, dev, stream)
+    ldo = _matrix(dh, "dh", (kind,), (M, N))
+    lddx = 0 if dx is None else _matrix(dx, "dx", (_BF16,), (M, N))
+    if dx is not None and kind is not _FP32:
+        raise ValueError("dx is written for a float32 stream only: dh is it")
+    size = 0
+    if dweight is not None:
+        _whole(dweight, "dweight", (_BF16, _FP32), (N,))
+        if workspace is None:
+            size = _lib().mx_rms_norm_backward_workspace_bytes(M, N)
+            if size > 0:
+                workspace = _empty((size,), _UINT8, dev, stream)
+        elif workspace.dtype is not _UINT8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        else:
+            size = workspace.numel()
+    _same_device(h, dy, dy2, weight, rstd, dh_in, dh, dx, dweight, workspace)
+    flags = (STREAM_FP32 if kind is _FP32 else 0) | (WEIGHT_FP32 if weight.dtype is _FP32 else 0)
+    _call("mx_rms_norm_backward", h.get_device(), stream, dy.data_ptr(), ldy, _at(dy2), ldy2, h.data_ptr(), ldh,
+          weight.data_ptr(), rstd.data_ptr(), _at(dh_in), ldi, M, N, flags, dh.data_ptr(), ldo, _at(dx), lddx,
+          _at(dweight), dweight is not None and dweight.dtype is _FP32, bool(accumulate), _at(workspace),
+          max(size, 0))
+    return dh, dx, dweight
+
+
+def mx_rms_norm_backward_workspace_bytes(M, N):
+    return int(_lib().mx_rms_norm_backward_workspace_bytes(int(M), int(N)))

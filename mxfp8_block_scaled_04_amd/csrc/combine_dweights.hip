@@ -1,0 +1,82 @@
+// Gradient of the routing weights through the combine:
+//   dw[t][i] = sum_n dout[t][n] y[slot(t, i)][n]
+// One workgroup per token: a lane has 8 columns of every 2048, holds them of
+// dout in registers and takes the token's rows 8 entries at a time (their
+// loads in flight together), one fp32 sum per entry; the sums are joined over
+// the lanes of a wave in registers and over the waves through LDS.
+#include "mx_bf16.h"
+#include "mx_block.h"
+#include "mx_device.h"
+#include "mx_lanes.h"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kEntries = 8;
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc = __builtin_fmaf(lo_bf16(aw[i]), lo_bf16(bw[i]), acc);
+        acc = __builtin_fmaf(hi_bf16(aw[i]), hi_bf16(bw[i]), acc);
+    }
+    return acc;
+}
+
+__global__ __launch_bounds__(kThreads) void combine_dweights_kernel(const uint16_t* __restrict__ dout, int64_t ldd,
+                                                                    const uint16_t* __restrict__ y, int64_t M,
+                                                                    int64_t ldy, const int32_t* __restrict__ slot_of,
+                                                                    int32_t k, int64_t N,
+                                                                    float* __restrict__ dweights) {
+    __shared__ float part[kWaves][kEntries];
+    const int64_t t = blockIdx.x;
+    const int wave = threadIdx.x >> 6;
+    for (int32_t i0 = 0; i0 < k; i0 += kEntries) {
+        float sum[kEntries];
+        int32_t slot[kEntries];
+#pragma unroll
+        for (int u = 0; u < kEntries; ++u) {
+            sum[u] = 0.0f;
+            slot[u] = i0 + u < k ? slot_of[t * k + i0 + u] : -1;
+        }
+        for (int64_t c = threadIdx.x * 8; c < N; c += kThreads * 8) {
+            const uint4 d = *reinterpret_cast<const uint4*>(dout + t * ldd + c);
+            uint4 v[kEntries];
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u) {
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (slot[u] >= 0 && slot[u] < M) v[u] = load_stream16(y + (int64_t)slot[u] * ldy + c);
+            }
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u)
+                if (slot[u] >= 0 && slot[u] < M) sum[u] = dot8(d, v[u], sum[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kEntries; ++u) {
+            sum[u] = team_sum<64>(sum[u]);
+            if ((threadIdx.x & 63) == 0) part[wave][u] = sum[u];
+        }
+        __syncthreads();
+        if (threadIdx.x < kEntries && i0 + (int)threadIdx.x < k) {
+            float all = 0.0f;
+            for (int w = 0; w < kWaves; ++w) all += part[w][threadIdx.x];
+            dweights[t * k + i0 + threadIdx.x] = all;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+hipError_t launch_combine_dweights(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t M, int64_t ldy,
+                                   const int32_t* slot_of, int64_t T, int32_t k, int64_t N, float* dweights,
+                                   hipStream_t stream) {
+    hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)T), dim3(kThreads), 0, stream, dout, ldd, y, M, ldy,
+                       slot_of, k, N, dweights);
+    return hipGetLastError();
+}
+
+}  // namespace mx

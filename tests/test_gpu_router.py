@@ -1,0 +1,395 @@
+"""The router and its gradient against the formulas in float64, at the sizes,
+masks, ties and types where they can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_block_scaled_04_amd as mx
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24  # half a step of float32, relative
+
+
+def _scores(l, score):
+    """float64 [T, E]; a row without finite logits has zeros."""
+    with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
+        if score == "sigmoid":
+            return np.where(l == -np.inf, 0.0, 1.0 / (1.0 + np.exp(-l)))
+        top = l.max(1, keepdims=True)
+        e = np.where(l == -np.inf, 0.0, np.exp(l - np.where(top == -np.inf, 0.0, top)))
+        total = e.sum(1, keepdims=True)
+        return np.divide(e, total, out=np.zeros_like(e), where=total != 0)
+
+
+def _order(values, available):
+    """Indices of the available values, largest first (NaN above all), ties by index."""
+    return sorted(np.flatnonzero(available), key=lambda e: (0 if np.isnan(values[e]) else 1, -values[e], e))
+
+
+def reference(logits, k, bias=None, groups=1, kept=None, top=2, score="softmax", renorm=True, scale=1.0):
+    l = logits.double().cpu().numpy()
+    T, E = l.shape
+    kept = groups if kept is None else kept
+    s = _scores(l, score)
+    # without a bias and with single choices per group the scores have the order of the logits
+    by_logit = bias is None and (groups == 1 or top == 1)
+    c = l.copy() if by_logit else s + (0.0 if bias is None else bias.double().cpu().numpy())
+    available = (l != -np.inf) & (c != -np.inf)
+    experts, weights = np.full((T, k), -1, np.int32), np.zeros((T, k))
+    size = E // groups
+    for t in range(T):
+        ok = available[t].copy()
+        if groups > 1:
+            total = np.zeros(groups)
+            for g in range(groups):
+                best = _order(c[t, g * size:(g + 1) * size], ok[g * size:(g + 1) * size])[:top]
+                total[g] = sum(c[t, g * size + e] for e in best)
+            some = ok.reshape(groups, size).any(1)
+            for g in set(range(groups)) - set(_order(total, some)[:kept]):
+                ok[g * size:(g + 1) * size] = False
+        chosen = _order(c[t], ok)[:k]
+        experts[t, :len(chosen)] = chosen
+        w = s[t, chosen]
+        if renorm:
+            w = w / w.sum() if w.sum() != 0 else w * 0
+        weights[t, :len(chosen)] = scale * w
+    return experts, weights, s
+
+
+def _logits(T, E, kind, seed, ld=None, spread=2.0):
+    gen = torch.Generator().manual_seed(seed)
+    l = (torch.randn((T, E), generator=gen) * spread).to(TYPES[kind])
+    if ld is None:
+        return l.cuda()
+    whole = torch.full((T, ld), float("nan"), dtype=TYPES[kind], device="cuda")
+    whole[:, :E] = l.cuda()
+    return whole[:, :E]
+
+
+def _check(logits, k, **kw):
+    scores = kw.pop("scores", True)
+    experts, weights, got = mx.mx_router(logits, k, scores=scores, **kw)
+    kw["kept"], kw["top"] = kw.pop("groups_kept", None), kw.pop("group_top", 2)
+    e, w, s = reference(logits, k, **kw)
+    assert np.array_equal(experts.cpu().numpy(), e)
+    # the sum of E exponentials in any order: E / 8 terms in a row at most, and 16 roundings besides
+    rel = U * (16 + logits.shape[1] / 8)
+    assert np.allclose(weights.cpu().numpy(), w, rtol=rel, atol=2.0 ** -126, equal_nan=True)
+    if got is not None:
+        assert np.allclose(got.cpu().numpy(), s, rtol=rel, atol=2.0 ** -126, equal_nan=True)
+    return experts, weights
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (65, 8, 2), (7, 9, 9), (33, 16, 8), (130, 60, 4), (5, 64, 64),
+                                   (64, 65, 7), (31, 128, 8), (17, 160, 6), (16, 256, 8), (9, 257, 16), (4, 512, 32),
+                                   (3, 1000, 33), (2, 2048, 64), (2, 4095, 10), (1, 4096, 64)])
+def test_choices_and_weights(T, E, k, score, kind):
+    l = _logits(T, E, kind, T + E + k)
+    _check(l, k, score=score)
+    _check(l, k, score=score, renorm=False, scale=2.5)
+    gen = torch.Generator().manual_seed(7)
+    bias = (0.3 * torch.randn(E, generator=gen)).cuda()
+    _check(l, k, score=score, bias=bias, scale=0.5)
+    _check(l, k, score=score, bias=torch.zeros(E).cuda(), renorm=False, scores=None)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,groups,kept,k", [(8, 8, 3, 3), (12, 3, 2, 5), (60, 4, 1, 15), (64, 2, 1, 32), (256, 8, 4, 8),
+                                             (165, 3, 2, 6), (35, 5, 5, 11), (64, 64, 9, 9), (128, 1, 1, 8),
+                                             (2046, 33, 20, 64), (4096, 64, 3, 17), (4096, 2, 1, 40)])
+def test_groups(E, groups, kept, k, top, score):
+    kind = "bf16" if E % 3 else "fp32"
+    l = _logits(19, E, kind, E + groups)
+    gen = torch.Generator().manual_seed(8)
+    bias = (0.3 * torch.randn(E, generator=gen)).cuda()
+    for b in (None, bias):
+        _check(l, k, groups=groups, groups_kept=kept, group_top=top, score=score, bias=b)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
+def test_ties_go_to_the_lowest_index(groups, kept, score, kind):
+    gen = torch.Generator().manual_seed(3)
+    l = torch.randint(-2, 3, (200, 64), generator=gen).to(TYPES[kind]).cuda()
+    l[0] = 0.0
+    bias = torch.randint(-1, 2, (64,), generator=gen).float().cuda() / 4
+    for b in (None, bias, torch.zeros(64).cuda()):
+        _check(l, 8, groups=groups, groups_kept=kept, score=score, bias=b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_that_float32_cannot_tell_apart(score):
+    """Pairs whose choices differ by a few 2^-40: by the formulas they are in order."""
+    T, E = 64, 32
+    gen = torch.Generator().manual_seed(4)
+    l = torch.randn((T, E), generator=gen)
+    s = torch.from_numpy(_scores(l.double().numpy(), score))
+    # one row's scores, cancelled by the bias: choices of that row are fp32 roundings of the bias
+    for t in (0, 5):
+        bias = (0.5 - s[t]).float().cuda()
+        _check(l.cuda(), 8, score=score, bias=bias)
+        _check(l.cuda(), 8, score=score, bias=bias, groups=4, groups_kept=2)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
+def test_masks(groups, kept, renorm, score, kind):
+    l = _logits(40, 32, kind, 11)
+    gen = torch.Generator().manual_seed(12)
+    l[torch.rand((40, 32), generator=gen).cuda() < 0.7] = -math.inf
+    l[0] = -math.inf                            # nothing left
+    l[1] = -math.inf
+    l[1, 17] = 0.5                              # one left
+    l[2] = torch.finfo(TYPES[kind]).min         # the lowest value is a value
+    l[3] = torch.finfo(TYPES[kind]).min
+    l[3, 4:6] = 1.0
+    l[4] = 88.0
+    l[5] = -300.0
+    bias = torch.zeros(32).cuda()
+    bias[9] = -math.inf                         # an expert taken out by its bias
+    for b in (None, bias):
+        experts, weights = _check(l, 6, groups=groups, groups_kept=kept, score=score, renorm=renorm, bias=b)
+        assert (experts[0] == -1).all() and (weights[0] == 0).all()
+        assert experts[1].tolist() == [17] + [-1] * 5
+        if b is not None:
+            assert not (experts == 9).any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_nan_and_infinities(with_bias, score):
+    l = _logits(6, 16, "fp32", 13)
+    l[0, 3] = math.nan
+    l[1, 5] = math.inf
+    l[2, 7], l[2, 2] = math.nan, -math.inf
+    bias = torch.zeros(16).cuda() if with_bias else None
+    experts, weights = (t.cpu() for t in mx.mx_router(l, 4, bias=bias, score=score)[:2])
+    assert ((experts >= 0) & (experts < 16)).all()
+    assert all(len(set(row.tolist())) == 4 for row in experts)
+    assert weights[0].isnan().all() and weights[2].isnan().all() and not (experts[2] == 2).any()
+    if score == "sigmoid":
+        assert experts[0, 0] == 3 and experts[2, 0] == 7 and experts[1, 0] == 5 and weights[1].isfinite().all()
+    else:
+        assert weights[1].isnan().all()
+    e, w, _ = reference(l[3:], 4, bias=bias, score=score)
+    assert np.array_equal(experts[3:].numpy(), e) and np.allclose(weights[3:].numpy(), w, rtol=18 * U)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("E,ld", [(16, 17), (33, 40), (256, 264), (256, 259)])
+def test_row_strides_and_unaligned_rows(E, ld, kind):
+    l = _logits(37, E, kind, 21, ld)
+    _check(l, 5, groups=1, score="sigmoid", bias=torch.linspace(0, 1, E).cuda())
+    _check(l[1:], 5)
+
+
+def test_no_tokens_and_rows_behind_the_last():
+    e, w, s = mx.mx_router(torch.zeros((0, 8), device="cuda"), 2, scores=True)
+    assert e.shape == (0, 2) and w.shape == (0, 2) and s.shape == (0, 8)
+    assert mx.mx_router_backward(torch.zeros((0, 8), device="cuda"), e, w).shape == (0, 8)
+    experts = torch.full((70, 3), 77, dtype=torch.int32, device="cuda")
+    weights, scores = torch.full((70, 3), 7.0, device="cuda"), torch.full((70, 8), 7.0, device="cuda")
+    l = _logits(67, 8, "bf16", 5)
+    mx.mx_router(l, 3, experts=experts[:67], weights=weights[:67], scores=scores[:67])
+    assert (experts[67:] == 77).all() and (weights[67:] == 7).all() and (scores[67:] == 7).all()
+    assert (experts[:67] != 77).all()
+    dl = torch.full((70, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_router_backward(l, experts[:67], weights[:67], dlogits=dl[:67])
+    assert (dl[67:] == 7).all()
+
+
+def test_rows_past_2_31_elements():
+    ld, E, T = 1 << 26, 24, 40
+    whole = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda")
+    l = whole.as_strided((T, E), (ld, 1))
+    l.copy_(_logits(T, E, "bf16", 6))
+    experts, weights = _check(l, 3)
+    g = torch.randn((T, 3), device="cuda")
+    want = mx.mx_router_backward(l.contiguous(), experts, g)
+    assert torch.equal(mx.mx_router_backward(l, experts, g, dlogits=l), want) and torch.equal(l, want)
+
+
+# -- gradient -----------------------------------------------------------------
+
+
+def reference_gradient(logits, experts, g, dscores, score, renorm, scale):
+    """(gradient, magnitude of what is added up in it), float64."""
+    l, g = logits.double().cpu().numpy(), g.double().cpu().numpy()
+    T, E = l.shape
+    s = _scores(l, score)
+    ds = np.zeros((T, E)) if dscores is None else dscores.double().cpu().numpy().copy()
+    mag = np.abs(ds)
+    for t in range(T):
+        at = [(i, e) for i, e in enumerate(experts[t].tolist()) if 0 <= e < E]
+        total = sum(s[t, e] for _, e in at)
+        mean = sum(g[t, i] * s[t, e] for i, e in at) / total if total else 0.0
+        size = sum(abs(g[t, i]) * s[t, e] for i, e in at) / total if total else 0.0
+        for i, e in at:
+            if renorm and total:
+                ds[t, e] += scale * (g[t, i] - mean) / total
+                mag[t, e] += abs(scale) * (abs(g[t, i]) + size) / total
+            elif not renorm:
+                ds[t, e] += scale * g[t, i]
+                mag[t, e] += abs(scale * g[t, i])
+    if score == "sigmoid":
+        return s * (1 - s) * ds, s * (1 - s) * mag, s
+    return (s * (ds - (s * ds).sum(1, keepdims=True)), s * (mag + (s * mag).sum(1, keepdims=True)), s)
+
+
+def _check_gradient(logits, experts, g, dscores=None, score="softmax", renorm=True, scale=1.0, **kw):
+    got = mx.mx_router_backward(logits, experts, g, dscores=dscores, score=score, renorm=renorm, scale=scale, **kw)
+    want, mag, s = reference_gradient(logits, experts, g, dscores, score, renorm, scale)
+    # fp32: sums over the choices (k) and over the experts (E / 8 in a row at most) and 40 roundings besides; 1 - s of a
+    # sigmoid near 1 is off by half a step of 1; the result is rounded to its type once
+    bound = mag * U * (40 + experts.shape[1] + logits.shape[1] / 8) + 2.0 ** -126
+    if score == "sigmoid":
+        bound += mag / np.maximum(1 - s, 1e-300) * 4 * U
+    bound += np.abs(want) * torch.finfo(logits.dtype).eps / 2
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= bound).all(), (err / bound).max()
+    return got
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (33, 8, 2), (130, 60, 4), (5, 64, 64), (17, 165, 6),
+                                   (64, 256, 8), (9, 257, 16), (2, 4095, 33), (2, 4096, 64), (31, 96, 3)])
+def test_gradient(T, E, k, renorm, score, kind):
+    l = _logits(T, E, kind, T + E)
+    gen = torch.Generator().manual_seed(1)
+    experts = mx.mx_router(l, k, score=score)[0]
+    g = torch.randn((T, k), generator=gen).cuda()
+    _check_gradient(l, experts, g, None, score, renorm, 2.5)
+    _check_gradient(l, experts, g, torch.randn((T, E), generator=gen).cuda() * 0.1, score, renorm, 2.5)
+    in_place = l.clone()
+    want = mx.mx_router_backward(l, experts, g, score=score, renorm=renorm)
+    assert torch.equal(mx.mx_router_backward(in_place, experts, g, score=score, renorm=renorm, dlogits=in_place), want)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_masks_drops_and_repeats(renorm, score, kind):
+    l = _logits(40, 32, kind, 31)
+    gen = torch.Generator().manual_seed(32)
+    l[torch.rand((40, 32), generator=gen).cuda() < 0.5] = -math.inf
+    l[0] = -math.inf
+    l[1] = torch.finfo(TYPES[kind]).min
+    l[2] = 60.0
+    experts = mx.mx_router(l, 5, score=score)[0]
+    experts[3, 1], experts[3, 3], experts[4, 0] = 32, -7, 1 << 30  # outside
+    experts[5] = experts[5, 0]                                     # the same one five times
+    experts[6] = -1                                                # none
+    experts[7, 1] = int((l[7] == -math.inf).nonzero()[0])          # a masked one
+    g = torch.randn((40, 5), generator=gen).cuda()
+    d = torch.randn((40, 32), generator=gen).cuda()
+    for dscores in (None, d):
+        got = _check_gradient(l, experts, g, dscores, score, renorm)
+        assert (got[l == -math.inf] == 0).all()
+        if dscores is None:
+            assert (got[6] == 0).all()
+
+
+@pytest.mark.parametrize("E,ld", [(16, 17), (33, 40), (256, 264), (256, 259)])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_gradient_row_strides(E, ld, kind):
+    l = _logits(37, E, kind, 21, ld)
+    experts = mx.mx_router(l, 5)[0]
+    g = torch.randn((37, 5), device="cuda")
+    out = torch.full((37, ld + 3), 9.0, dtype=TYPES[kind], device="cuda")
+    _check_gradient(l, experts, g, None, "sigmoid", True, dlogits=out[:, 1:E + 1])
+    assert (out[:, 0] == 9).all() and (out[:, E + 1:] == 9).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_against_differences(renorm, score):
+    """d/dl of sum(g w) + sum(d s) by central differences of mx_router's own outputs."""
+    T, E, k = 6, 12, 3
+    l = torch.linspace(-2, 2, E).repeat(T, 1)
+    gen = torch.Generator().manual_seed(2)
+    l = l.gather(1, torch.rand((T, E), generator=gen).argsort(1)).cuda()  # gaps of 0.36: the choice stays
+    g, d = torch.randn((T, k), generator=gen).double().cuda(), torch.randn((T, E), generator=gen).double().cuda()
+
+    def value(l):
+        _, w, s = mx.mx_router(l, k, score=score, renorm=renorm, scale=1.5, scores=True)
+        return (w.double() * g).sum(1) + (s.double() * d).sum(1)
+
+    experts = mx.mx_router(l, k, score=score)[0]
+    got = mx.mx_router_backward(l, experts, g.float(), dscores=d.float(), score=score, renorm=renorm, scale=1.5)
+    h = 2.0 ** -5
+    for e in range(E):
+        up, down = l.clone(), l.clone()
+        up[:, e] += h
+        down[:, e] -= h
+        diff = (value(up) - value(down)) / (2 * h)
+        # third derivatives are at most about as large as the sums of |g| and |d|: h^2 / 6 of them; fp32 noise below
+        bound = (g.abs().sum(1) * 1.5 + d.abs().sum(1)) * (h * h / 6 + 16 * U / h)
+        assert ((diff - got[:, e].double()).abs() <= bound).all()
+
+
+# -- streams and graphs -----------------------------------------------------------
+
+
+def test_captured_and_replayed():
+    l = _logits(300, 64, "bf16", 41)
+    bias = torch.zeros(64).cuda()
+    g = torch.randn((300, 4), device="cuda")
+    outs = [torch.zeros((300, 4), dtype=torch.int32, device="cuda"), torch.zeros((300, 4), device="cuda"),
+            torch.zeros((300, 64), dtype=torch.bfloat16, device="cuda")]
+
+    def step(e, w, dl):
+        mx.mx_router(l, 4, bias=bias, groups=4, groups_kept=2, score="sigmoid", experts=e, weights=w)
+        mx.mx_router_backward(l, e, g, score="sigmoid", dlogits=dl)
+
+    step(*[o.clone() for o in outs])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*outs)
+    for seed in range(4):
+        l.copy_(_logits(300, 64, "bf16", 50 + seed))
+        want = [torch.zeros_like(o) for o in outs]
+        step(*want)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_on_another_stream():
+    l = _logits(5000, 256, "fp32", 61)
+    want = mx.mx_router(l, 8, scores=True)
+    g = torch.randn((5000, 8), device="cuda")
+    dwant = mx.mx_router_backward(l, want[0], g)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    freed = torch.empty_like(want[1])
+    at = freed.data_ptr()
+    del freed
+    got = mx.mx_router(l, 8, scores=True, stream=side)
+    assert got[1].data_ptr() != at
+    dgot = mx.mx_router_backward(l, got[0], g, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(dgot, dwant)
+
+
+def test_the_plan_takes_what_the_router_writes():
+    """Masked tokens are dropped by the plan; the others' counts add up."""
+    l = _logits(257, 16, "fp32", 71)
+    l[10] = -math.inf
+    l[11, 1:] = -math.inf
+    experts, weights, _ = mx.mx_router(l, 3)
+    offsets, src, slot_of, _ = mx.mx_route_plan(experts, 16, weights)
+    assert int(offsets[-1]) == 257 * 3 - 3 - 2
+    assert (slot_of[10] == -1).all() and (slot_of[11] >= 0).tolist() == [True, False, False]
