@@ -36,7 +36,7 @@ enum {
  * Router: for each token t with logits l[e], e < E,
  *   s[e] = e^l[e] / sum e^l, or 1 / (1 + e^-l[e])      the scores
  *   c[e] = s[e] + bias[e] (c = s without a bias)        the choices
- * An expert whose logit or choice is -infinity (a mask) is never chosen.
+ * An expert whose logit or bias is -infinity (a mask) is never chosen.
  * With groups > 1 the experts form groups of E / groups consecutive ones; a
  * group's score is the sum of its group_top largest choices (of one, if only
  * one expert of it can be chosen), and only experts of the groups_kept groups

@@ -13,7 +13,7 @@ template <int D>
 __device__ __forceinline__ uint32_t other_half(uint32_t v) {
     static_assert(D == 1 || D == 2 || D == 4 || D == 8, "inside a row of 16 lanes");
     constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;  // quad_perm, half mirror, mirror
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xF, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true);  // (no lane reads outside its row)
 }
 
 // op(v, v of the other half) with op commutative; T of 4 or 8 bytes.

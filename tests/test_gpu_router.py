@@ -38,7 +38,7 @@ def reference(logits, k, bias=None, groups=1, kept=None, top=2, score="softmax",
     # without a bias and with single choices per group the scores have the order of the logits
     by_logit = bias is None and (groups == 1 or top == 1)
     c = l.copy() if by_logit else s + (0.0 if bias is None else bias.double().cpu().numpy())
-    available = (l != -np.inf) & (c != -np.inf)
+    available = (l != -np.inf) & (True if bias is None else bias.cpu().numpy() != -np.inf)
     experts, weights = np.full((T, k), -1, np.int32), np.zeros((T, k))
     size = E // groups
     for t in range(T):
@@ -123,6 +123,44 @@ def test_ties_go_to_the_lowest_index(groups, kept, score, kind):
     bias = torch.randint(-1, 2, (64,), generator=gen).float().cuda() / 4
     for b in (None, bias, torch.zeros(64).cuda()):
         _check(l, 8, groups=groups, groups_kept=kept, score=score, bias=b)
+
+
+def test_zeros_of_both_signs_are_a_tie():
+    l = torch.zeros((4, 64), device="cuda")
+    l[:, ::2] = -0.0
+    l[1:] -= (torch.rand((3, 64), generator=torch.Generator().manual_seed(1)) < 0.5).cuda().float()
+    experts, _ = _check(l, 8)
+    assert experts[0].tolist() == list(range(8))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(64, 8), (512, 8), (4096, 32)])
+def test_few_distinct_values(E, k, score):
+    """Rows of one, two and three values, and rows with fewer open experts than choices."""
+    l = torch.zeros((12, E), device="cuda")
+    gen = torch.Generator().manual_seed(9)
+    for t in range(1, 6):
+        l[t] = torch.randint(0, t, (E,), generator=gen).float().cuda()
+    l[6:] = -math.inf
+    for t in range(6, 12):
+        l[t, torch.randperm(E, generator=gen)[:2 * (t - 6)].cuda()] = 1.0
+    for b in (None, torch.zeros(E).cuda()):
+        _check(l, k, score=score, bias=b)
+        _check(l, k, score=score, bias=b, groups=4, groups_kept=3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_far_from_one(score):
+    """Logits whose scores underflow in float32, or that are all far from 0."""
+    l = _logits(30, 128, "fp32", 14)
+    l[:10] -= 95.0
+    l[10:15] += 60.0
+    l[15:20] *= 40.0
+    l[20] = -500.0 - torch.arange(128, device="cuda")
+    bias = (torch.randn(128, generator=torch.Generator().manual_seed(3)) * 1e-4).cuda()
+    for b in (None, bias, torch.zeros(128).cuda()):
+        _check(l, 8, score=score, bias=b)
+        _check(l, 8, score=score, bias=b, groups=8, groups_kept=4)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -242,18 +280,17 @@ def reference_gradient(logits, experts, g, dscores, score, renorm, scale):
                 ds[t, e] += scale * g[t, i]
                 mag[t, e] += abs(scale * g[t, i])
     if score == "sigmoid":
-        return s * (1 - s) * ds, s * (1 - s) * mag, s
-    return (s * (ds - (s * ds).sum(1, keepdims=True)), s * (mag + (s * mag).sum(1, keepdims=True)), s)
+        rest = _scores(-l, "sigmoid")  # 1 - s, where the difference would cancel
+        return s * rest * ds, s * rest * mag
+    return (s * (ds - (s * ds).sum(1, keepdims=True)), s * (mag + (s * mag).sum(1, keepdims=True)))
 
 
 def _check_gradient(logits, experts, g, dscores=None, score="softmax", renorm=True, scale=1.0, **kw):
     got = mx.mx_router_backward(logits, experts, g, dscores=dscores, score=score, renorm=renorm, scale=scale, **kw)
-    want, mag, s = reference_gradient(logits, experts, g, dscores, score, renorm, scale)
-    # fp32: sums over the choices (k) and over the experts (E / 8 in a row at most) and 40 roundings besides; 1 - s of a
-    # sigmoid near 1 is off by half a step of 1; the result is rounded to its type once
+    want, mag = reference_gradient(logits, experts, g, dscores, score, renorm, scale)
+    # fp32: sums over the choices (k) and over the experts (E / 8 in a row at most) and 40 roundings besides; the result is
+    # rounded to its type once
     bound = mag * U * (40 + experts.shape[1] + logits.shape[1] / 8) + 2.0 ** -126
-    if score == "sigmoid":
-        bound += mag / np.maximum(1 - s, 1e-300) * 4 * U
     bound += np.abs(want) * torch.finfo(logits.dtype).eps / 2
     err = np.abs(got.double().cpu().numpy() - want)
     assert (err <= bound).all(), (err / bound).max()
