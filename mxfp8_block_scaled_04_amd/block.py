@@ -12,8 +12,9 @@ import ctypes
 
 import torch
 
-from . import _check, load, mx_scale_bytes
-from .training import _empty, _same_device
+from . import _check, load
+from .training import _empty as _empty_on
+from .training import _same_device
 
 SIGMOID, RENORM, LOGITS_BF16 = 1, 2, 4
 STREAM_FP32, WEIGHT_FP32 = 1, 2
@@ -51,39 +52,65 @@ def _lib():
     return lib
 
 
+# Small calls are bound by the host's part, so the checks below avoid what
+# costs a microsecond each: stream and device objects (the raw handle is read
+# where this torch has it), tests of what a call has made itself.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(name, at, stream, *args):
     """The call on GPU `at`, which need not be the current one."""
-    if stream is None:
-        handle = torch.cuda.current_stream(at).cuda_stream
-    elif stream.device.index != at:
-        raise ValueError("the stream is of another GPU than the tensors")
-    else:
+    if stream is not None:
+        if stream.device.index != at:
+            raise ValueError("the stream is of another GPU than the tensors")
         handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(at)
+    else:
+        handle = torch.cuda.current_stream(at).cuda_stream
     f = getattr(_lib(), name)
     if at == torch.cuda.current_device():
         rc = f(*args, handle)
     else:
         with torch.cuda.device(at):
             rc = f(*args, handle)
-    _check(rc, name)
+    if rc:
+        _check(rc, name)
 
 
-def _matrix(t, name, dtypes, shape=None):
-    """The row stride of a matrix whose rows are contiguous."""
+def _empty(rows, columns, dtype, device, stream):
+    if stream is None:
+        return torch.empty(rows, columns, dtype=dtype, device=device)
+    return _empty_on((rows, columns), dtype, device, stream)
+
+
+def _vector(length, dtype, device, stream):
+    return torch.empty(length, dtype=dtype, device=device) if stream is None else _empty_on(length, dtype, device, stream)
+
+
+def _wrong_type(t, name, dtypes):
+    return TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, not {t.dtype}")
+
+
+def _matrix(t, name, dtypes, rows=None, columns=None):
+    """The row stride of a matrix (of rows x columns, if given) whose rows are contiguous."""
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, not {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be a matrix" + ("" if shape is None else f" of {shape[0]} x {shape[1]}"))
-    rows, columns = t.shape
-    if columns > 1 and t.stride(1) != 1:
+        raise _wrong_type(t, name, dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    r, c = t.shape
+    if rows is not None and (r != rows or c != columns):
+        raise ValueError(f"{name} must be a matrix of {rows} x {columns}")
+    ld, step = t.stride()
+    if step != 1 and c > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return 8 * -(-columns // 8) if rows <= 1 or columns == 0 else t.stride(0)  # (not used)
+    return 8 * -(-c // 8) if r <= 1 or c == 0 else ld  # (not used)
 
 
-def _whole(t, name, dtypes, shape):
+def _whole(t, name, dtypes, *shape):
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise _wrong_type(t, name, dtypes)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {' x '.join(map(str, shape))}")
 
 
@@ -112,18 +139,21 @@ def mx_router(logits, k, bias=None, groups=1, groups_kept=None, group_top=2, sco
     ldl = _matrix(logits, "logits", (_FP32, _BF16))
     T, E = logits.shape
     flags = _flags(score, renorm, logits)
+    dev = logits.device
     if experts is None:
-        experts = _empty((T, k), _INT32, logits.device, stream)
+        experts = _empty(T, k, _INT32, dev, stream)
+    else:
+        _whole(experts, "experts", (_INT32,), T, k)
     if weights is None:
-        weights = _empty((T, k), _FP32, logits.device, stream)
+        weights = _empty(T, k, _FP32, dev, stream)
+    else:
+        _whole(weights, "weights", (_FP32,), T, k)
     if scores is True:
-        scores = _empty((T, E), _FP32, logits.device, stream)
-    _whole(experts, "experts", (_INT32,), (T, k))
-    _whole(weights, "weights", (_FP32,), (T, k))
-    if scores is not None:
-        _whole(scores, "scores", (_FP32,), (T, E))
+        scores = _empty(T, E, _FP32, dev, stream)
+    elif scores is not None:
+        _whole(scores, "scores", (_FP32,), T, E)
     if bias is not None:
-        _whole(bias, "bias", (_FP32,), (E,))
+        _whole(bias, "bias", (_FP32,), E)
     _same_device(logits, bias, experts, weights, scores)
     _call("mx_router", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, _at(bias), groups,
           groups if groups_kept is None else groups_kept, group_top, k, scale, flags, experts.data_ptr(),
@@ -140,14 +170,16 @@ def mx_router_backward(logits, experts, dweights, dscores=None, score="softmax",
     ldl = _matrix(logits, "logits", (_FP32, _BF16))
     T, E = logits.shape
     k = experts.shape[1] if experts.dim() == 2 else 0
-    _whole(experts, "experts", (_INT32,), (T, k))
-    _whole(dweights, "dweights", (_FP32,), (T, k))
+    _whole(experts, "experts", (_INT32,), T, k)
+    _whole(dweights, "dweights", (_FP32,), T, k)
     if dscores is not None:
-        _whole(dscores, "dscores", (_FP32,), (T, E))
+        _whole(dscores, "dscores", (_FP32,), T, E)
     flags = _flags(score, renorm, logits)
+    ldd = E
     if dlogits is None:
-        dlogits = _empty((T, E), logits.dtype, logits.device, stream)
-    ldd = _matrix(dlogits, "dlogits", (logits.dtype,), (T, E))
+        dlogits = _empty(T, E, logits.dtype, logits.device, stream)
+    else:
+        ldd = _matrix(dlogits, "dlogits", (logits.dtype,), T, E)
     _same_device(logits, experts, dweights, dscores, dlogits)
     _call("mx_router_backward", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, experts.data_ptr(),
           dweights.data_ptr(), _at(dscores), k, scale, flags, dlogits.data_ptr(), ldd)
@@ -160,12 +192,13 @@ def mx_combine_dweights(dout, y, slot_of, dweights=None, stream=None):
     of each token's output gradient with its expert rows (0 where it has none)."""
     ldd = _matrix(dout, "dout", (_BF16,))
     T, N = dout.shape
-    ldy = _matrix(y, "y", (_BF16,), (y.shape[0], N))
+    ldy = _matrix(y, "y", (_BF16,), y.shape[0], N)
     k = slot_of.shape[1] if slot_of.dim() == 2 else 0
-    _whole(slot_of, "slot_of", (_INT32,), (T, k))
+    _whole(slot_of, "slot_of", (_INT32,), T, k)
     if dweights is None:
-        dweights = _empty((T, k), _FP32, dout.device, stream)
-    _whole(dweights, "dweights", (_FP32,), (T, k))
+        dweights = _empty(T, k, _FP32, dout.device, stream)
+    else:
+        _whole(dweights, "dweights", (_FP32,), T, k)
     _same_device(dout, y, slot_of, dweights)
     _call("mx_combine_dweights", dout.get_device(), stream, dout.data_ptr(), ldd, y.data_ptr(), y.shape[0], ldy,
           slot_of.data_ptr(), T, k, N, dweights.data_ptr())
@@ -181,35 +214,39 @@ def mx_rms_norm(x, weight, residual=None, eps=1e-6, h=None, y=True, q=None, s=No
     rstd float32 [M] for the backward pass.  h: the sum, allocated with a
     residual if None; it may be the residual itself.  Returns (y, h, q, s, rstd);
     h is None without a residual."""
+    M, N = x.shape if x.dim() == 2 else (0, 0)
+    dev, ldh, ldy = x.device, N, N
     if residual is None:
         ldx, ldr, kind = _matrix(x, "x", (_BF16, _FP32)), 0, x.dtype
         if h is not None:
             raise ValueError("h is written with a residual only")
     else:
-        ldx, ldr = _matrix(x, "x", (_BF16,)), _matrix(residual, "residual", (_BF16, _FP32), tuple(x.shape))
-        kind = residual.dtype
-    M, N = x.shape
-    dev = x.device
-    _whole(weight, "weight", (_BF16, _FP32), (N,))
-    if residual is not None and h is None:
-        h = _empty((M, N), kind, dev, stream)
+        ldx, ldr, kind = _matrix(x, "x", (_BF16,)), _matrix(residual, "residual", (_BF16, _FP32), M, N), residual.dtype
+        if h is None:
+            h = _empty(M, N, kind, dev, stream)
+        else:
+            ldh = _matrix(h, "h", (kind,), M, N)
+    _whole(weight, "weight", (_BF16, _FP32), N)
     if y is True:
-        y = _empty((M, N), _BF16, dev, stream)
-    if q is None and s is not None:
-        raise ValueError("s is written with q only")
-    if q is True:
-        q = _empty((M, N), _UINT8, dev, stream)
-    if q is not None and (s is None or s is True):
-        s = _empty((mx_scale_bytes(M, N),), _UINT8, dev, stream)
-    if rstd is True:
-        rstd = _empty((M,), _FP32, dev, stream)
-    ldh = 0 if h is None else _matrix(h, "h", (kind,), (M, N))
-    ldy = 0 if y is None else _matrix(y, "y", (_BF16,), (M, N))
+        y = _empty(M, N, _BF16, dev, stream)
+    elif y is not None:
+        ldy = _matrix(y, "y", (_BF16,), M, N)
     if q is not None:
-        _whole(q, "q", (_UINT8,), (M, N))
-        _whole(s, "s", (_UINT8,), (mx_scale_bytes(M, N),))
-    if rstd is not None:
-        _whole(rstd, "rstd", (_FP32,), (M,))
+        size = 32 * -(-M // 32) * 8 * -(-N // 256)  # mx_scale_bytes
+        if q is True:
+            q = _empty(M, N, _UINT8, dev, stream)
+        else:
+            _whole(q, "q", (_UINT8,), M, N)
+        if s is None or s is True:
+            s = _vector(size, _UINT8, dev, stream)
+        else:
+            _whole(s, "s", (_UINT8,), size)
+    elif s is not None:
+        raise ValueError("s is written with q only")
+    if rstd is True:
+        rstd = _vector(M, _FP32, dev, stream)
+    elif rstd is not None:
+        _whole(rstd, "rstd", (_FP32,), M)
     _same_device(x, residual, weight, h, y, q, s, rstd)
     flags = (STREAM_FP32 if kind is _FP32 else 0) | (WEIGHT_FP32 if weight.dtype is _FP32 else 0)
     _call("mx_rms_norm", x.get_device(), stream, x.data_ptr(), ldx, _at(residual), ldr, weight.data_ptr(), M, N, eps,
@@ -230,31 +267,35 @@ def mx_rms_norm_backward(dy, h, weight, rstd, dy2=None, dh_in=None, dh=None, dx=
     None."""
     ldh = _matrix(h, "h", (_BF16, _FP32))
     M, N = h.shape
-    kind, dev = h.dtype, h.device
-    ldy = _matrix(dy, "dy", (_BF16,), (M, N))
-    ldy2 = 0 if dy2 is None else _matrix(dy2, "dy2", (_BF16,), (M, N))
-    ldi = 0 if dh_in is None else _matrix(dh_in, "dh_in", (kind,), (M, N))
-    _whole(weight, "weight", (_BF16, _FP32), (N,))
-    _whole(rstd, "rstd", (_FP32,), (M,))
+    kind, dev, ldo, lddx = h.dtype, h.device, N, N
+    ldy = _matrix(dy, "dy", (_BF16,), M, N)
+    ldy2 = 0 if dy2 is None else _matrix(dy2, "dy2", (_BF16,), M, N)
+    ldi = 0 if dh_in is None else _matrix(dh_in, "dh_in", (kind,), M, N)
+    _whole(weight, "weight", (_BF16, _FP32), N)
+    _whole(rstd, "rstd", (_FP32,), M)
     if dh is None:
-        dh = _empty((M, N), kind, dev, stream)
-    if dx is True:
-        dx = _empty((M, N), _BF16, dev, stream)
-    if accumulate and not isinstance(dweight, torch.Tensor):
-        raise ValueError("accumulate needs dweight")
-    if dweight is True or isinstance(dweight, torch.dtype):
-        dweight = _empty((N,), weight.dtype if dweight is True else dweight, dev, stream)
-    ldo = _matrix(dh, "dh", (kind,), (M, N))
-    lddx = 0 if dx is None else _matrix(dx, "dx", (_BF16,), (M, N))
-    if dx is not None and kind is not _FP32:
-        raise ValueError("dx is written for a float32 stream only: dh is it")
+        dh = _empty(M, N, kind, dev, stream)
+    else:
+        ldo = _matrix(dh, "dh", (kind,), M, N)
+    if dx is not None:
+        if kind is not _FP32:
+            raise ValueError("dx is written for a float32 stream only: dh is it")
+        if dx is True:
+            dx = _empty(M, N, _BF16, dev, stream)
+        else:
+            lddx = _matrix(dx, "dx", (_BF16,), M, N)
     size = 0
+    if isinstance(dweight, torch.Tensor):
+        _whole(dweight, "dweight", (_BF16, _FP32), N)
+    elif accumulate:
+        raise ValueError("accumulate needs dweight")
+    elif dweight is not None:
+        dweight = _vector(N, weight.dtype if dweight is True else dweight, dev, stream)
     if dweight is not None:
-        _whole(dweight, "dweight", (_BF16, _FP32), (N,))
         if workspace is None:
             size = _lib().mx_rms_norm_backward_workspace_bytes(M, N)
             if size > 0:
-                workspace = _empty((size,), _UINT8, dev, stream)
+                workspace = _vector(size, _UINT8, dev, stream)
         elif workspace.dtype is not _UINT8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor")
         else:

@@ -9,6 +9,8 @@
 // One pass: a row stays in the registers of its team of lanes, 8 columns a
 // lane and vector, from the loads to the stores; the sum over the row is a
 // reduction in registers and, for teams of several waves, LDS.
+#include <type_traits>
+
 #include "mx_bf16.h"
 #include "mx_block.h"
 #include "mx_device.h"
@@ -61,6 +63,15 @@ __device__ __forceinline__ float row_sum(float v, float* buffer) {
     for (int w = 0; w < waves; ++w) all += buffer[w];
     return all;
 }
+
+// Vectors of 8 columns a lane has, and the workgroup's threads, of rows that a workgroup has alone.
+constexpr int64_t kTeamVectors = 256;  // up to here a wave has a row
+int block_vectors(int64_t vectors) { return vectors <= 64 * kMaxWaves ? 1 : vectors <= 2 * 64 * kMaxWaves ? 2 : 4; }
+int block_threads(int64_t vectors) {
+    const int V = block_vectors(vectors);
+    return (int)((vectors + 64 * V - 1) / (64 * V)) * 64;
+}
+int team_lanes(int64_t vectors) { return vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64; }
 
 // S: the stream's type, WT: the weight's (uint16_t: bf16).
 template <class S, class WT, int LANES, int V>
@@ -148,109 +159,190 @@ hipError_t pick_norm(const NormArgs& g, hipStream_t stream) {
     if (vectors <= 32) return run_norm<S, WT, 32, 1>(g, 256, stream);
     if (vectors <= 64) return run_norm<S, WT, 64, 1>(g, 256, stream);
     if (vectors <= 128) return run_norm<S, WT, 64, 2>(g, 256, stream);
-    const auto threads = [&](int V) { return (int)((vectors + 64 * V - 1) / (64 * V)) * 64; };
-    if (vectors <= 64 * kMaxWaves) return run_norm<S, WT, 0, 1>(g, threads(1), stream);
-    if (vectors <= 2 * 64 * kMaxWaves) return run_norm<S, WT, 0, 2>(g, threads(2), stream);
-    return run_norm<S, WT, 0, 4>(g, threads(4), stream);
+    if (vectors <= 192) return run_norm<S, WT, 64, 3>(g, 256, stream);
+    if (vectors <= kTeamVectors) return run_norm<S, WT, 64, 4>(g, 256, stream);
+    const int threads = block_threads(vectors);
+    if (block_vectors(vectors) == 1) return run_norm<S, WT, 0, 1>(g, threads, stream);
+    if (block_vectors(vectors) == 2) return run_norm<S, WT, 0, 2>(g, threads, stream);
+    return run_norm<S, WT, 0, 4>(g, threads, stream);
 }
 
 // ---------------------------------------------------------------------------
 // Backward.  Persistent workgroups take rows with a stride of the grid and
-// hold the sums of g z for their columns in registers; each writes one row of
-// partial sums, which a second kernel adds up in order.
+// hold the sums of g z for their columns in registers (the row's loads are
+// issued before the row in front of it is finished); the teams of a workgroup
+// are added up in LDS, each workgroup writes one row of partial sums, and a
+// second kernel adds these up in order.
 // ---------------------------------------------------------------------------
 
-template <class S, class WT, int V>
-__global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_kernel(NormBackwardArgs g) {
+// A row's values as they are loaded.
+template <class S, int V>
+struct Row {
+    typedef typename std::conditional<sizeof(S) == 2, uint4, Eight>::type Wide;
+    uint4 dy[V], dy2[V];
+    Wide h[V], in[V];
+    float r;
+};
+__device__ __forceinline__ Eight values(uint4 d) { return unpack(d); }
+__device__ __forceinline__ Eight values(const Eight& e) { return e; }
+__device__ __forceinline__ void raw8(const uint16_t* p, uint4& d) { d = *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void raw8(const float* p, Eight& d) { d = load8(p); }
+
+template <class S, int V>
+__device__ __forceinline__ void load_row(const NormBackwardArgs& g, int64_t row, bool live, int first, int step,
+                                         Row<S, V>& x) {
+    x.r = live ? g.rstd[row] : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = first + v * step;
+        x.dy[v] = x.dy2[v] = make_uint4(0, 0, 0, 0);
+        x.h[v] = typename Row<S, V>::Wide{};
+        x.in[v] = typename Row<S, V>::Wide{};
+        if (!live || c >= g.N) continue;
+        raw8((const S*)g.h + row * g.ldh + c, x.h[v]);
+        raw8(g.dy + row * g.ldy + c, x.dy[v]);
+        if (g.dy2 != nullptr) raw8(g.dy2 + row * g.ldy2 + c, x.dy2[v]);
+        if (g.dh_in != nullptr) raw8((const S*)g.dh_in + row * g.ldi + c, x.in[v]);
+    }
+}
+
+constexpr int kTeamThreads = 256;  // of a workgroup of several teams
+
+template <class S, class WT, int LANES, int V>
+__global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void norm_backward_kernel(NormBackwardArgs g) {
     __shared__ float buffer[2][kMaxWaves];
+    const int team = LANES > 0 ? LANES : blockDim.x;
+    const int a = LANES > 0 ? threadIdx.x & (LANES - 1) : threadIdx.x;
+    constexpr int kTeams = LANES > 0 ? kTeamThreads / (LANES > 0 ? LANES : 1) : 1;
+    const int64_t mine = LANES > 0 ? threadIdx.x / LANES : 0;
     const int64_t N = g.N;
+    const int first = a * 8, step = team * 8;
     Eight dw[V], w[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t c = (int64_t)(v * blockDim.x + threadIdx.x) * 8;
         dw[v] = Eight{};
         w[v] = Eight{};
-        if (c < N) w[v] = load8((const WT*)g.weight + c);
+        if (first + v * step < N) w[v] = load8((const WT*)g.weight + first + v * step);
     }
+    const int64_t stride = (int64_t)gridDim.x * kTeams;
+    int64_t row = (int64_t)blockIdx.x * kTeams + mine;
+    Row<S, V> next;
+    load_row<S, V>(g, row, row < g.M, first, step, next);
     int turn = 0;
-    for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x, turn ^= 1) {
-        const float r = g.rstd[row];
+    for (int64_t r0 = (int64_t)blockIdx.x * kTeams; r0 < g.M; r0 += stride, row += stride, turn ^= 1) {
+        const bool live = row < g.M;
+        const float r = next.r;
         Eight z[V], e[V];
+        typename Row<S, V>::Wide in[V];
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * blockDim.x + threadIdx.x) * 8;
-            z[v] = Eight{};
-            e[v] = Eight{};
-            if (c < N) {
-                z[v] = load8((const S*)g.h + row * g.ldh + c);
-                e[v] = load8(g.dy + row * g.ldy + c);
-                if (g.dy2 != nullptr) {
-                    const Eight more = load8(g.dy2 + row * g.ldy2 + c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[v].v[i] += more.v[i];
-                }
-            }
+            z[v] = values(next.h[v]);
+            e[v] = unpack(next.dy[v]);
+            const Eight more = unpack(next.dy2[v]);
+            in[v] = next.in[v];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                if (g.dy2 != nullptr) e[v].v[i] += more.v[i];
                 z[v].v[i] *= r;
                 dw[v].v[i] = __builtin_fmaf(e[v].v[i], z[v].v[i], dw[v].v[i]);
                 e[v].v[i] *= w[v].v[i];
                 sum = __builtin_fmaf(e[v].v[i], z[v].v[i], sum);
             }
         }
-        const float mean = row_sum<0>(sum, buffer[turn]) / (float)N;
+        if (V <= 2) load_row<S, V>(g, row + stride, row + stride < g.M, first, step, next);
+        const float mean = row_sum<LANES>(sum, buffer[turn]) / (float)N;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * blockDim.x + threadIdx.x) * 8;
-            if (c >= N) continue;
-            Eight in{};
-            if (g.dh_in != nullptr) in = load8((const S*)g.dh_in + row * g.ldi + c);
+            const int64_t c = first + v * step;
+            if (!live || c >= N) continue;
+            const Eight from = values(in[v]);
             Eight out;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) out.v[i] = in.v[i] + r * (e[v].v[i] - z[v].v[i] * mean);
+            for (int i = 0; i < 8; ++i) out.v[i] = from.v[i] + r * (e[v].v[i] - z[v].v[i] * mean);
             if (g.dx != nullptr) store16(g.dx + row * g.lddx + c, pack(out));
             store8((S*)g.dh + row * g.ldo + c, out);
         }
+        if (V > 2) load_row<S, V>(g, row + stride, row + stride < g.M, first, step, next);
     }
     if (g.dweight == nullptr) return;
+    float* const part = g.workspace + (int64_t)blockIdx.x * N;
+    if constexpr (LANES == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t c = (int64_t)(v * blockDim.x + threadIdx.x) * 8;
-        if (c < N) store8(g.workspace + (int64_t)blockIdx.x * N + c, dw[v]);
+        for (int v = 0; v < V; ++v)
+            if (first + v * step < N) store8(part + first + v * step, dw[v]);
+    } else {
+        __shared__ float sums[kTeams][LANES * 8 * V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums[mine][first + v * step + i] = dw[v].v[i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < N; c += kTeamThreads) {
+            float all = 0.0f;
+#pragma unroll
+            for (int t = 0; t < kTeams; ++t) all += sums[t][c];
+            part[c] = all;
+        }
     }
 }
 
-__global__ __launch_bounds__(256) void norm_dweight_kernel(const float* __restrict__ part, int32_t parts, int64_t N,
-                                                           void* __restrict__ dweight, bool fp32, bool accumulate) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= N) return;
+// Columns [COLUMNS b, ...) of the parts' sum: 1024 / COLUMNS threads share the
+// parts of a column out, then add up in LDS.
+template <int COLUMNS>
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restrict__ part, int32_t parts, int64_t N,
+                                                            void* __restrict__ dweight, bool fp32, bool accumulate) {
+    constexpr int kShares = 1024 / COLUMNS;
+    __shared__ float sums[kShares][COLUMNS + 1];
+    const int column = threadIdx.x % COLUMNS, share = threadIdx.x / COLUMNS;
+    const int64_t c = (int64_t)blockIdx.x * COLUMNS + column;
     float sum = 0.0f;
-    for (int32_t p = 0; p < parts; ++p) sum += part[(int64_t)p * N + c];
+    if (c < N) {
+#pragma unroll 8
+        for (int32_t p = share; p < parts; p += kShares) sum += part[(int64_t)p * N + c];
+    }
+    sums[share][column] = sum;
+    for (int half = kShares / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (share < half) sums[share][column] += sums[share + half][column];
+    }
+    if (share != 0 || c >= N) return;
+    sum = sums[0][column];
     if (!fp32)
         ((uint16_t*)dweight)[c] = __builtin_bit_cast(uint16_t, (__bf16)sum);
     else
         ((float*)dweight)[c] = accumulate ? ((float*)dweight)[c] + sum : sum;
 }
 
+template <class S, class WT, int LANES, int V>
+void run_rows(const NormBackwardArgs& g, int32_t parts, int threads, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_backward_kernel<S, WT, LANES, V>), dim3(parts), dim3(threads), 0, stream, g);
+}
+
 template <class S, class WT>
 hipError_t run_backward(const NormBackwardArgs& g, hipStream_t stream) {
     const int32_t parts = norm_backward_parts(g.M, g.N);
     if (parts > 0) {
-        const int64_t vectors = g.N / 8;
-        const auto threads = [&](int V) { return (int)((vectors + 64 * V - 1) / (64 * V)) * 64; };
-        if (vectors <= 64 * kMaxWaves)
-            hipLaunchKernelGGL((norm_backward_kernel<S, WT, 1>), dim3(parts), dim3(threads(1)), 0, stream, g);
-        else if (vectors <= 2 * 64 * kMaxWaves)
-            hipLaunchKernelGGL((norm_backward_kernel<S, WT, 2>), dim3(parts), dim3(threads(2)), 0, stream, g);
-        else
-            hipLaunchKernelGGL((norm_backward_kernel<S, WT, 4>), dim3(parts), dim3(threads(4)), 0, stream, g);
+        const int64_t n = g.N / 8;
+        if (n <= 16) run_rows<S, WT, 16, 1>(g, parts, kTeamThreads, stream);
+        else if (n <= 32) run_rows<S, WT, 32, 1>(g, parts, kTeamThreads, stream);
+        else if (n <= 64) run_rows<S, WT, 64, 1>(g, parts, kTeamThreads, stream);
+        else if (n <= 128) run_rows<S, WT, 64, 2>(g, parts, kTeamThreads, stream);
+        else if (n <= 192) run_rows<S, WT, 64, 3>(g, parts, kTeamThreads, stream);
+        else if (n <= kTeamVectors) run_rows<S, WT, 64, 4>(g, parts, kTeamThreads, stream);
+        else if (block_vectors(n) == 1) run_rows<S, WT, 0, 1>(g, parts, block_threads(n), stream);
+        else if (block_vectors(n) == 2) run_rows<S, WT, 0, 2>(g, parts, block_threads(n), stream);
+        else run_rows<S, WT, 0, 4>(g, parts, block_threads(n), stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (g.dweight == nullptr) return hipSuccess;
-    hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((g.N + 255) / 256)), dim3(256), 0, stream, g.workspace,
-                       parts, g.N, g.dweight, g.dw_fp32, g.accumulate);
+    if (g.N <= 1024)
+        hipLaunchKernelGGL((norm_dweight_kernel<8>), dim3((unsigned)((g.N + 7) / 8)), dim3(1024), 0, stream, g.workspace,
+                           parts, g.N, g.dweight, g.dw_fp32, g.accumulate);
+    else
+        hipLaunchKernelGGL((norm_dweight_kernel<32>), dim3((unsigned)((g.N + 31) / 32)), dim3(1024), 0, stream,
+                           g.workspace, parts, g.N, g.dweight, g.dw_fp32, g.accumulate);
     return hipGetLastError();
 }
 
@@ -263,8 +355,11 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
 }
 
 int32_t norm_backward_parts(int64_t M, int64_t N) {
-    (void)N;
-    return (int32_t)(M < 512 ? M : 512);
+    const int64_t n = N / 8;
+    const int64_t rows = n <= kTeamVectors ? kTeamThreads / team_lanes(n) : 1;  // that a workgroup takes at a time
+    const int64_t threads = n <= kTeamVectors ? kTeamThreads : block_threads(n);
+    const int64_t most = 256 * (2048 / threads), wanted = (M + rows - 1) / rows;  // as many as the 256 CUs hold
+    return (int32_t)(wanted < most ? wanted : most);
 }
 
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
