@@ -6,9 +6,20 @@
 // quantize_rows_kernel has it.  Backward with g = dy + dy2, a = g w, z = h r:
 // dh = dh_in + r (a - z mean(a z)), dw = sum over rows of g z.
 //
-// One pass: a row stays in the registers of its team of lanes, 8 columns a
-// lane and vector, from the loads to the stores; the sum over the row is a
-// reduction in registers and, for teams of several waves, LDS.
+// What bounds it: HBM.  A row stays in the registers of its team of lanes, 8
+// columns a lane and vector, from the loads to the stores, so that everything
+// is read and written once; the sum over the row is a reduction in registers
+// and, where a workgroup is the team, LDS.  Measured on 32768 rows of 7168,
+// bf16: forward with residual and MXFP8 rows (9.03 bytes an element)
+// 353 us, 6.0 TB/s; backward with both output gradients and the
+// stream's (10 bytes) 415 us, 5.7 TB/s; a copy reaches 5.1
+// TB/s, the 2:1 stream of mx_stream21 6.6.
+//
+// Teams: a wave, half, a quarter or an eighth of one for rows of up to 1024,
+// 256, 128 and 64 columns (no barrier); a workgroup for longer ones (2048
+// columns: 173 us forward and backward, with a wave 186 and 213).  1.3 10^8
+// elements, bf16 without MXFP8: 5.5 to 6.2 TB/s forward and 5.0 to 6.2 backward
+// from 64 to 16384 columns; float32 streams 5.2 to 5.9.
 #include <type_traits>
 
 #include "mx_bf16.h"
@@ -31,25 +42,53 @@ __device__ __forceinline__ uint4 pack(const Eight& e) {
     return make_uint4(pack_bf16(e.v[0], e.v[1]), pack_bf16(e.v[2], e.v[3]), pack_bf16(e.v[4], e.v[5]),
                       pack_bf16(e.v[6], e.v[7]));
 }
-__device__ __forceinline__ Eight load8(const uint16_t* p) { return unpack(*reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ Eight load8(const float* p) {
+__device__ __forceinline__ uint4 four(const Eight& e, int i) {
+    return __builtin_bit_cast(uint4, make_float4(e.v[i], e.v[i + 1], e.v[i + 2], e.v[i + 3]));
+}
+
+// Eight values of a row as they are loaded: bf16 stay packed until they are used.
+template <class S>
+using Raw = typename std::conditional<sizeof(S) == 2, uint4, Eight>::type;
+__device__ __forceinline__ Eight values(uint4 d) { return unpack(d); }
+__device__ __forceinline__ const Eight& values(const Eight& e) { return e; }
+
+// Rows are read once: non-temporal loads (forward as above 410 -> 370 us).
+// Not of float32, where an instruction takes every other 16 bytes: the second
+// one finds its lines in the cache then (8192 columns, residual in float32: 303
+// -> 287 us; the stores as well, 505 -> 303).
+__device__ __forceinline__ uint4 load_raw(const uint16_t* p) { return load_stream16(p); }
+__device__ __forceinline__ Eight load_raw(const float* p) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     return Eight{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
+// The weight is read for every row.
+__device__ __forceinline__ Eight load_kept(const uint16_t* p) { return unpack(*reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ Eight load_kept(const float* p) { return load_raw(p); }
+
+// Outputs of large calls leave the caches before anything reads them: from
+// 2^25 elements on, where a call's rows pass the 256 MB of the Infinity Cache,
+// their stores are non-temporal (forward 370 -> 353 us, backward 454 -> 415);
+// smaller ones are left where the next kernel finds them.
+constexpr int64_t kFar = (int64_t)1 << 25;
+__device__ __forceinline__ void store_out(void* p, uint4 d, bool far) {
+    if (far) store_stream16(p, d);
+    else store16(p, d);
+}
 // Rounded to the stream's type, in place, and stored.
-__device__ __forceinline__ void store8(uint16_t* p, Eight& e) {
+__device__ __forceinline__ void store_row(uint16_t* p, Eight& e, bool far) {
     const uint4 d = pack(e);
-    *reinterpret_cast<uint4*>(p) = d;
+    store_out(p, d, far);
     e = unpack(d);
 }
-__device__ __forceinline__ void store8(float* p, Eight& e) {
-    *reinterpret_cast<float4*>(p) = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
+__device__ __forceinline__ void store_row(float* p, Eight& e, bool) {
+    store16(p, four(e, 0));
+    store16(p + 4, four(e, 4));
 }
 
 constexpr int kMaxWaves = 16;
+constexpr int kTeamThreads = 256;  // of a workgroup of several teams
 
-// The team's sum in all of its lanes.  LANES: 16, 32, 64 (several teams per
+// The team's sum in all of its lanes.  LANES: 8, 16, 32, 64 (several teams per
 // workgroup), or 0: the workgroup is the team (`buffer`: one float per wave,
 // another one in the next call, so that one barrier is enough).
 template <int LANES>
@@ -64,26 +103,40 @@ __device__ __forceinline__ float row_sum(float v, float* buffer) {
     return all;
 }
 
-// Vectors of 8 columns a lane has, and the workgroup's threads, of rows that a workgroup has alone.
-constexpr int64_t kTeamVectors = 256;  // up to here a wave has a row
-int block_vectors(int64_t vectors) { return vectors <= 64 * kMaxWaves ? 1 : vectors <= 2 * 64 * kMaxWaves ? 2 : 4; }
-int block_threads(int64_t vectors) {
-    const int V = block_vectors(vectors);
-    return (int)((vectors + 64 * V - 1) / (64 * V)) * 64;
+// A team for rows of `vectors` times 8 columns.
+struct Shape {
+    int lanes;    // of a wave, or 0: a workgroup
+    int vectors;  // per lane
+    int threads;  // of a workgroup
+    int teams;    // in it
+};
+// The forward pass: a lane of a workgroup has 1, 2 or 4 vectors (4096 columns:
+// 169, 176, 182 us; 8192: 185, 176, 182).  The backward pass, whose rows take
+// more registers: 1 up to 8192 columns.
+Shape shape_of(int64_t vectors, int64_t most_of_one) {
+    for (int lanes = 8; lanes <= 64; lanes *= 2)
+        if (vectors <= lanes) return Shape{lanes, 1, kTeamThreads, kTeamThreads / lanes};
+    if (vectors <= 128) return Shape{64, 2, kTeamThreads, kTeamThreads / 64};
+    const int each = vectors <= most_of_one ? 1 : vectors <= 2 * 64 * kMaxWaves ? 2 : 4;
+    return Shape{0, each, (int)((vectors + 64 * each - 1) / (64 * each)) * 64, 1};
 }
-int team_lanes(int64_t vectors) { return vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64; }
 
 // S: the stream's type, WT: the weight's (uint16_t: bf16).
 template <class S, class WT, int LANES, int V>
-__global__ __launch_bounds__(LANES > 0 ? 256 : 64 * kMaxWaves) void rms_norm_kernel(NormArgs g, int64_t rows) {
+__global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void rms_norm_kernel(NormArgs g, int64_t rows,
+                                                                                             bool far) {
     __shared__ float buffer[2][kMaxWaves];
+    constexpr int kTeams = LANES > 0 ? kTeamThreads / (LANES > 0 ? LANES : 1) : 1;
     const int team = LANES > 0 ? LANES : blockDim.x;
     const int a = LANES > 0 ? threadIdx.x & (LANES - 1) : threadIdx.x;
-    const int64_t teams = LANES > 0 ? 256 / LANES : 1;
     const int64_t mine = LANES > 0 ? threadIdx.x / LANES : 0;
     const int64_t N = g.N;
+    // Workgroups go round the 8 XCDs: 32 rows in a row to each, so that the 4-byte pieces of a unit of scales meet in one L2
+    // (364 -> 355 us).
+    int64_t block = blockIdx.x;
+    if (LANES == 0 && (block | 255) < gridDim.x) block = (block & ~(int64_t)255) + (block % 8) * 32 + (block % 256) / 8;
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < rows; r0 += (int64_t)gridDim.x * teams, turn ^= 1) {
+    for (int64_t r0 = block * kTeams; r0 < rows; r0 += (int64_t)gridDim.x * kTeams, turn ^= 1) {
         const int64_t row = r0 + mine;
         const bool live = row < g.M;
         Eight h[V];
@@ -94,13 +147,13 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 64 * kMaxWaves) void rms_norm_ker
             h[v] = Eight{};
             if (live && c < N) {
                 if (g.residual != nullptr) {
-                    h[v] = load8((const uint16_t*)g.x + row * g.ldx + c);
-                    const Eight r = load8((const S*)g.residual + row * g.ldr + c);
+                    h[v] = unpack(load_raw((const uint16_t*)g.x + row * g.ldx + c));
+                    const Eight r = values(load_raw((const S*)g.residual + row * g.ldr + c));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) h[v].v[i] += r.v[i];
-                    store8((S*)g.h + row * g.ldh + c, h[v]);
+                    store_row((S*)g.h + row * g.ldh + c, h[v], far);
                 } else {
-                    h[v] = load8((const S*)g.x + row * g.ldx + c);
+                    h[v] = values(load_raw((const S*)g.x + row * g.ldx + c));
                 }
             }
 #pragma unroll
@@ -115,22 +168,28 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 64 * kMaxWaves) void rms_norm_ker
             const int64_t c = (int64_t)(v * team + a) * 8;
             uint4 out = make_uint4(0, 0, 0, 0);
             if (live && c < N) {
-                const Eight w = load8((const WT*)g.weight + c);
+                const Eight w = load_kept((const WT*)g.weight + c);
                 Eight e;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) e.v[i] = h[v].v[i] * r * w.v[i];
                 out = pack(e);
-                if (g.y != nullptr) store16(g.y + row * g.ldy + c, out);
+                if (g.y != nullptr) store_out(g.y + row * g.ldy + c, out, far);
             }
             if (g.q == nullptr) continue;
             const uint32_t scale = scale_from_maxmag(quad_max_u32(max_mag8(out)));
-            if (live && c < N) mx::store8(g.q + row * N + c, quant8(out, scale));
+            if (live && c < N) {
+                const uint2 codes = quant8(out, scale);
+                if (far) store_stream8(g.q + row * N + c, codes);
+                else store8(g.q + row * N + c, codes);
+            }
             // the unit's scale bytes of this row: two dwords, of the even and
             // the odd blocks, byte b / 2; 4 lanes have a block, 32 a unit
-            const int in_unit = threadIdx.x & (LANES == 16 ? 15 : 31), b = in_unit >> 2;
+            constexpr int kUnit = LANES == 8 || LANES == 16 ? LANES : 32;
+            const int in_unit = threadIdx.x & (kUnit - 1), b = in_unit >> 2;
             uint32_t word = scale << (8 * (b >> 1));
-            word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x128, 0xF, 0xF, false);  // row_ror:8 (block b ^ 2)
-            if constexpr (LANES != 16) {
+            if constexpr (kUnit >= 16)
+                word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x128, 0xF, 0xF, false);  // row_ror:8 (block b ^ 2)
+            if constexpr (kUnit == 32) {
                 const auto p = __builtin_amdgcn_permlane16_swap(word, word, false, false);  // block b ^ 4
                 word = p[0] | p[1];
             }
@@ -143,134 +202,149 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 64 * kMaxWaves) void rms_norm_ker
 }
 
 template <class S, class WT, int LANES, int V>
-hipError_t run_norm(const NormArgs& g, int threads, hipStream_t stream) {
+hipError_t run_norm(const NormArgs& g, const Shape& at, hipStream_t stream) {
     const int64_t rows = g.q != nullptr ? (g.M + 31) / 32 * 32 : g.M;  // with the padding rows of the scales
-    const int64_t teams = LANES > 0 ? 256 / LANES : 1;
-    int64_t blocks = (rows + teams - 1) / teams;
+    int64_t blocks = (rows + at.teams - 1) / at.teams;
     if (blocks > (1 << 20)) blocks = 1 << 20;
-    hipLaunchKernelGGL((rms_norm_kernel<S, WT, LANES, V>), dim3((unsigned)blocks), dim3(threads), 0, stream, g, rows);
+    hipLaunchKernelGGL((rms_norm_kernel<S, WT, LANES, V>), dim3((unsigned)blocks), dim3(at.threads), 0, stream, g, rows,
+                       g.M * g.N >= kFar);
     return hipGetLastError();
 }
 
 template <class S, class WT>
 hipError_t pick_norm(const NormArgs& g, hipStream_t stream) {
-    const int64_t vectors = g.N / 8;
-    if (vectors <= 16) return run_norm<S, WT, 16, 1>(g, 256, stream);
-    if (vectors <= 32) return run_norm<S, WT, 32, 1>(g, 256, stream);
-    if (vectors <= 64) return run_norm<S, WT, 64, 1>(g, 256, stream);
-    if (vectors <= 128) return run_norm<S, WT, 64, 2>(g, 256, stream);
-    if (vectors <= 192) return run_norm<S, WT, 64, 3>(g, 256, stream);
-    if (vectors <= kTeamVectors) return run_norm<S, WT, 64, 4>(g, 256, stream);
-    const int threads = block_threads(vectors);
-    if (block_vectors(vectors) == 1) return run_norm<S, WT, 0, 1>(g, threads, stream);
-    if (block_vectors(vectors) == 2) return run_norm<S, WT, 0, 2>(g, threads, stream);
-    return run_norm<S, WT, 0, 4>(g, threads, stream);
+    const Shape at = shape_of(g.N / 8, 512);
+    switch (at.lanes + at.vectors) {
+        case 8 + 1: return run_norm<S, WT, 8, 1>(g, at, stream);
+        case 16 + 1: return run_norm<S, WT, 16, 1>(g, at, stream);
+        case 32 + 1: return run_norm<S, WT, 32, 1>(g, at, stream);
+        case 64 + 1: return run_norm<S, WT, 64, 1>(g, at, stream);
+        case 64 + 2: return run_norm<S, WT, 64, 2>(g, at, stream);
+        case 0 + 1: return run_norm<S, WT, 0, 1>(g, at, stream);
+        case 0 + 2: return run_norm<S, WT, 0, 2>(g, at, stream);
+        default: return run_norm<S, WT, 0, 4>(g, at, stream);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // Backward.  Persistent workgroups take rows with a stride of the grid and
-// hold the sums of g z for their columns in registers (the row's loads are
-// issued before the row in front of it is finished); the teams of a workgroup
-// are added up in LDS, each workgroup writes one row of partial sums, and a
-// second kernel adds these up in order.
+// hold the sums of g z for their columns in registers; the teams of a
+// workgroup are added up in LDS, each workgroup writes one row of partial
+// sums, and a second kernel adds these up in order (5 us at 7168 columns).
+// Two workgroups per CU: more take as long or longer, and write more parts
+// (2048 columns: 173, 181 and 194 us with 2, 3 and 4).
+//
+// AHEAD: the next row's loads are issued before this row is finished, and the
+// weight is kept.  Without it neither, and dh_in is read after the sum, so that
+// 2 workgroups of up to 16 waves fit a CU: above 4096 columns (7168: 415 us
+// against 430; 4096: 193 against 182).
 // ---------------------------------------------------------------------------
 
-// A row's values as they are loaded.
-template <class S, int V>
+// A row's values as they are loaded; nothing where there is no row.
+template <class S, int V, bool AHEAD>
 struct Row {
-    typedef typename std::conditional<sizeof(S) == 2, uint4, Eight>::type Wide;
     uint4 dy[V], dy2[V];
-    Wide h[V], in[V];
+    Raw<S> h[V], in[AHEAD ? V : 1];
     float r;
-};
-__device__ __forceinline__ Eight values(uint4 d) { return unpack(d); }
-__device__ __forceinline__ Eight values(const Eight& e) { return e; }
-__device__ __forceinline__ void raw8(const uint16_t* p, uint4& d) { d = *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void raw8(const float* p, Eight& d) { d = load8(p); }
-
-template <class S, int V>
-__device__ __forceinline__ void load_row(const NormBackwardArgs& g, int64_t row, bool live, int first, int step,
-                                         Row<S, V>& x) {
-    x.r = live ? g.rstd[row] : 0.0f;
+    __device__ __forceinline__ void load(const NormBackwardArgs& g, int64_t row, int first, int step) {
+        const bool live = row < g.M;
+        r = live ? g.rstd[row] : 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t c = first + v * step;
-        x.dy[v] = x.dy2[v] = make_uint4(0, 0, 0, 0);
-        x.h[v] = typename Row<S, V>::Wide{};
-        x.in[v] = typename Row<S, V>::Wide{};
-        if (!live || c >= g.N) continue;
-        raw8((const S*)g.h + row * g.ldh + c, x.h[v]);
-        raw8(g.dy + row * g.ldy + c, x.dy[v]);
-        if (g.dy2 != nullptr) raw8(g.dy2 + row * g.ldy2 + c, x.dy2[v]);
-        if (g.dh_in != nullptr) raw8((const S*)g.dh_in + row * g.ldi + c, x.in[v]);
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = first + v * step;
+            dy[v] = dy2[v] = make_uint4(0, 0, 0, 0);
+            h[v] = Raw<S>{};
+            if constexpr (AHEAD) in[v] = Raw<S>{};
+            if (!live || c >= g.N) continue;
+            h[v] = load_raw((const S*)g.h + row * g.ldh + c);
+            dy[v] = load_raw(g.dy + row * g.ldy + c);
+            if (g.dy2 != nullptr) dy2[v] = load_raw(g.dy2 + row * g.ldy2 + c);
+            if constexpr (AHEAD)
+                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c);
+        }
     }
-}
+    // z, and g in e
+    __device__ __forceinline__ void take(const NormBackwardArgs& a, int v, Eight& z, Eight& e) const {
+        z = values(h[v]);
+        e = unpack(dy[v]);
+        const Eight more = unpack(dy2[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (a.dy2 != nullptr) e.v[i] += more.v[i];
+            z.v[i] *= r;
+        }
+    }
+};
 
-constexpr int kTeamThreads = 256;  // of a workgroup of several teams
-
-template <class S, class WT, int LANES, int V>
-__global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void norm_backward_kernel(NormBackwardArgs g) {
+template <class S, class WT, int LANES, int V, bool AHEAD>
+__global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void norm_backward_kernel(NormBackwardArgs g,
+                                                                                                  bool far) {
     __shared__ float buffer[2][kMaxWaves];
+    constexpr int kTeams = LANES > 0 ? kTeamThreads / (LANES > 0 ? LANES : 1) : 1;
     const int team = LANES > 0 ? LANES : blockDim.x;
     const int a = LANES > 0 ? threadIdx.x & (LANES - 1) : threadIdx.x;
-    constexpr int kTeams = LANES > 0 ? kTeamThreads / (LANES > 0 ? LANES : 1) : 1;
     const int64_t mine = LANES > 0 ? threadIdx.x / LANES : 0;
     const int64_t N = g.N;
     const int first = a * 8, step = team * 8;
-    Eight dw[V], w[V];
+    const auto weight = [&](int v) {
+        const int c = first + v * step;
+        return c < N ? load_kept((const WT*)g.weight + c) : Eight{};
+    };
+    Eight dw[V], kept[AHEAD ? V : 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         dw[v] = Eight{};
-        w[v] = Eight{};
-        if (first + v * step < N) w[v] = load8((const WT*)g.weight + first + v * step);
+        if constexpr (AHEAD) kept[v] = weight(v);
     }
     const int64_t stride = (int64_t)gridDim.x * kTeams;
     int64_t row = (int64_t)blockIdx.x * kTeams + mine;
-    Row<S, V> next;
-    load_row<S, V>(g, row, row < g.M, first, step, next);
+    Row<S, V, AHEAD> x;
+    if constexpr (AHEAD) x.load(g, row, first, step);
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * kTeams; r0 < g.M; r0 += stride, row += stride, turn ^= 1) {
-        const bool live = row < g.M;
-        const float r = next.r;
         Eight z[V], e[V];
-        typename Row<S, V>::Wide in[V];
+        Raw<S> in[V];
         float sum = 0.0f;
+        if constexpr (!AHEAD) x.load(g, row, first, step);
+        const float r = x.r;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            z[v] = values(next.h[v]);
-            e[v] = unpack(next.dy[v]);
-            const Eight more = unpack(next.dy2[v]);
-            in[v] = next.in[v];
+            x.take(g, v, z[v], e[v]);
+            if constexpr (AHEAD) in[v] = x.in[v];
+            Eight w;
+            if constexpr (AHEAD) w = kept[v];
+            else w = weight(v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (g.dy2 != nullptr) e[v].v[i] += more.v[i];
-                z[v].v[i] *= r;
                 dw[v].v[i] = __builtin_fmaf(e[v].v[i], z[v].v[i], dw[v].v[i]);
-                e[v].v[i] *= w[v].v[i];
+                e[v].v[i] *= w.v[i];
                 sum = __builtin_fmaf(e[v].v[i], z[v].v[i], sum);
             }
         }
-        if (V <= 2) load_row<S, V>(g, row + stride, row + stride < g.M, first, step, next);
+        if constexpr (AHEAD) x.load(g, row + stride, first, step);
         const float mean = row_sum<LANES>(sum, buffer[turn]) / (float)N;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = first + v * step;
-            if (!live || c >= N) continue;
+            if (row >= g.M || c >= N) continue;
+            if constexpr (!AHEAD) {
+                in[v] = Raw<S>{};
+                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c);
+            }
             const Eight from = values(in[v]);
             Eight out;
 #pragma unroll
             for (int i = 0; i < 8; ++i) out.v[i] = from.v[i] + r * (e[v].v[i] - z[v].v[i] * mean);
-            if (g.dx != nullptr) store16(g.dx + row * g.lddx + c, pack(out));
-            store8((S*)g.dh + row * g.ldo + c, out);
+            if (g.dx != nullptr) store_out(g.dx + row * g.lddx + c, pack(out), far);
+            store_row((S*)g.dh + row * g.ldo + c, out, far);
         }
-        if (V > 2) load_row<S, V>(g, row + stride, row + stride < g.M, first, step, next);
     }
     if (g.dweight == nullptr) return;
     float* const part = g.workspace + (int64_t)blockIdx.x * N;
     if constexpr (LANES == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (first + v * step < N) store8(part + first + v * step, dw[v]);
+            if (first + v * step < N) store_row(part + first + v * step, dw[v], false);
     } else {
         __shared__ float sums[kTeams][LANES * 8 * V];
 #pragma unroll
@@ -287,8 +361,60 @@ __global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void nor
     }
 }
 
+// Rows above 16384 columns: their values do not fit the registers (kept, they
+// spill: 500 us at 32768 columns, 314 here).  The sums of g z are in LDS, and
+// a row is read again after its sum.
+template <class S, class WT>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_long_kernel(NormBackwardArgs g, bool far) {
+    __shared__ __attribute__((aligned(16))) float dw[MX_NORM_MAX_N];  // (a thread uses its own columns only)
+    __shared__ float buffer[2][kMaxWaves];
+    const int N = (int)g.N, first = threadIdx.x * 8, step = blockDim.x * 8;
+    const auto columns = [&](int c) { return reinterpret_cast<float4*>(dw + c); };
+    for (int c = first; c < N; c += step) columns(c)[0] = columns(c)[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x, turn ^= 1) {
+        float sum = 0.0f;
+#pragma unroll 2
+        for (int c = first; c < N; c += step) {
+            Row<S, 1, false> x;
+            x.load(g, row, c, 0);
+            Eight z, e;
+            x.take(g, 0, z, e);
+            const Eight w = load_kept((const WT*)g.weight + c);
+            Eight d = load_kept(dw + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d.v[i] = __builtin_fmaf(e.v[i], z.v[i], d.v[i]);
+                sum = __builtin_fmaf(e.v[i] * w.v[i], z.v[i], sum);
+            }
+            columns(c)[0] = make_float4(d.v[0], d.v[1], d.v[2], d.v[3]);
+            columns(c)[1] = make_float4(d.v[4], d.v[5], d.v[6], d.v[7]);
+        }
+        const float mean = row_sum<0>(sum, buffer[turn]) / (float)N;
+#pragma unroll 2
+        for (int c = first; c < N; c += step) {
+            Row<S, 1, true> x;
+            x.load(g, row, c, 0);
+            Eight z, e;
+            x.take(g, 0, z, e);
+            const Eight w = load_kept((const WT*)g.weight + c), from = values(x.in[0]);
+            Eight out;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out.v[i] = from.v[i] + x.r * (e.v[i] * w.v[i] - z.v[i] * mean);
+            if (g.dx != nullptr) store_out(g.dx + row * g.lddx + c, pack(out), far);
+            store_row((S*)g.dh + row * g.ldo + c, out, far);
+        }
+    }
+    if (g.dweight == nullptr) return;
+    for (int c = first; c < N; c += step) {
+        Eight d = load_kept(dw + c);
+        store_row(g.workspace + (int64_t)blockIdx.x * N + c, d, false);
+    }
+}
+
 // Columns [COLUMNS b, ...) of the parts' sum: 1024 / COLUMNS threads share the
-// parts of a column out, then add up in LDS.
+// parts of a column out, then add up in LDS.  8 columns where there are few (a
+// workgroup for each), else 32 (whole lines of the parts).
 template <int COLUMNS>
 __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restrict__ part, int32_t parts, int64_t N,
                                                             void* __restrict__ dweight, bool fp32, bool accumulate) {
@@ -314,25 +440,34 @@ __global__ __launch_bounds__(1024) void norm_dweight_kernel(const float* __restr
         ((float*)dweight)[c] = accumulate ? ((float*)dweight)[c] + sum : sum;
 }
 
-template <class S, class WT, int LANES, int V>
-void run_rows(const NormBackwardArgs& g, int32_t parts, int threads, hipStream_t stream) {
-    hipLaunchKernelGGL((norm_backward_kernel<S, WT, LANES, V>), dim3(parts), dim3(threads), 0, stream, g);
+constexpr int64_t kBackwardOne = 64 * kMaxWaves;  // rows of up to so many vectors: one per lane
+
+template <class S, class WT, int LANES, int V, bool AHEAD>
+void run_rows(const NormBackwardArgs& g, const Shape& at, int32_t parts, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_backward_kernel<S, WT, LANES, V, AHEAD>), dim3(parts), dim3(at.threads), 0, stream, g,
+                       g.M * g.N >= kFar);
 }
 
 template <class S, class WT>
 hipError_t run_backward(const NormBackwardArgs& g, hipStream_t stream) {
     const int32_t parts = norm_backward_parts(g.M, g.N);
     if (parts > 0) {
-        const int64_t n = g.N / 8;
-        if (n <= 16) run_rows<S, WT, 16, 1>(g, parts, kTeamThreads, stream);
-        else if (n <= 32) run_rows<S, WT, 32, 1>(g, parts, kTeamThreads, stream);
-        else if (n <= 64) run_rows<S, WT, 64, 1>(g, parts, kTeamThreads, stream);
-        else if (n <= 128) run_rows<S, WT, 64, 2>(g, parts, kTeamThreads, stream);
-        else if (n <= 192) run_rows<S, WT, 64, 3>(g, parts, kTeamThreads, stream);
-        else if (n <= kTeamVectors) run_rows<S, WT, 64, 4>(g, parts, kTeamThreads, stream);
-        else if (block_vectors(n) == 1) run_rows<S, WT, 0, 1>(g, parts, block_threads(n), stream);
-        else if (block_vectors(n) == 2) run_rows<S, WT, 0, 2>(g, parts, block_threads(n), stream);
-        else run_rows<S, WT, 0, 4>(g, parts, block_threads(n), stream);
+        const Shape at = shape_of(g.N / 8, kBackwardOne);
+        switch (at.lanes + at.vectors) {
+            case 8 + 1: run_rows<S, WT, 8, 1, true>(g, at, parts, stream); break;
+            case 16 + 1: run_rows<S, WT, 16, 1, true>(g, at, parts, stream); break;
+            case 32 + 1: run_rows<S, WT, 32, 1, true>(g, at, parts, stream); break;
+            case 64 + 1: run_rows<S, WT, 64, 1, true>(g, at, parts, stream); break;
+            case 64 + 2: run_rows<S, WT, 64, 2, true>(g, at, parts, stream); break;
+            case 0 + 1:
+                if (at.threads <= 512) run_rows<S, WT, 0, 1, true>(g, at, parts, stream);
+                else run_rows<S, WT, 0, 1, false>(g, at, parts, stream);
+                break;
+            case 0 + 2: run_rows<S, WT, 0, 2, false>(g, at, parts, stream); break;
+            default:
+                hipLaunchKernelGGL((norm_backward_long_kernel<S, WT>), dim3(parts), dim3(at.threads), 0, stream, g,
+                                   g.M * g.N >= kFar);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -355,10 +490,10 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
 }
 
 int32_t norm_backward_parts(int64_t M, int64_t N) {
-    const int64_t n = N / 8;
-    const int64_t rows = n <= kTeamVectors ? kTeamThreads / team_lanes(n) : 1;  // that a workgroup takes at a time
-    const int64_t threads = n <= kTeamVectors ? kTeamThreads : block_threads(n);
-    const int64_t most = 256 * (2048 / threads), wanted = (M + rows - 1) / rows;  // as many as the 256 CUs hold
+    const Shape at = shape_of(N / 8, kBackwardOne);
+    // on each of 256 CUs one workgroup of 9 to 16 waves with many registers or much LDS, four of 3, two of others
+    const int64_t most = at.lanes > 0 ? 512 : at.vectors > 1 ? 256 : at.threads <= 192 ? 1024 : 512;
+    const int64_t wanted = (M + at.teams - 1) / at.teams;
     return (int32_t)(wanted < most ? wanted : most);
 }
 
