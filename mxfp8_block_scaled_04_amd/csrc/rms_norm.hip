@@ -491,9 +491,13 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
 
 int32_t norm_backward_parts(int64_t M, int64_t N) {
     const Shape at = shape_of(N / 8, kBackwardOne);
-    // on each of 256 CUs one workgroup of 9 to 16 waves with many registers or much LDS, four of 3, two of others
-    const int64_t most = at.lanes > 0 ? 512 : at.vectors > 1 ? 256 : at.threads <= 192 ? 1024 : 512;
-    const int64_t wanted = (M + at.teams - 1) / at.teams;
+    const int64_t wanted = (M + at.teams - 1) / at.teams;  // one step of rows each
+    // On each of 256 CUs one workgroup of many registers or much LDS, two of others (1531 rows of 1480, float32 stream: 256
+    // parts 12.4 us, 384 12.8, 512 11.8, 1024 14.2), and four of 3 waves where there are rows for them (8192: 25.1 -> 24.4).
+    int64_t most = 512;
+    if (at.lanes == 0 && at.vectors > 1) most = 256;
+    else if (at.lanes == 0 && at.threads <= 192 && wanted >= 8192) most = 1024;
+    if (wanted < most) most = 256;
     return (int32_t)(wanted < most ? wanted : most);
 }
 
