@@ -1,8 +1,8 @@
 """One MoE layer's expert computation on one GPU, forward and backward, as a
 chain of libmxmoe calls.  MoELayer takes token rows already grouped by
 expert; RoutedMoELayer (at the end) adds the route plan, the dispatch and the
-combine around it for top-k routed tokens (no router: the expert choices and
-weights are inputs).  This is the layer-level view of the public
+combine around it for top-k routed tokens (the expert choices and weights are
+inputs: moe_block.MoEBlock has the router).  This is the layer-level view of the public
 write-ups on Cursor's MXFP8 MoE kernels (aigc.bar "被忽视的量化税": the
 quantization passes next to the grouped GEMMs of a layer; lpnh.cn 2479732
 section 1: the forward and backward passes and the transposed quantization
@@ -254,7 +254,8 @@ class RoutedMoELayer:
           weight, quantize both ways (in place of B1)      mx_gather_quantize
       B2 .. B6 as MoELayer
       D'  reverse dispatch: dX[t] = sum_j dx[slot(t, j)]   mx_combine
-    The routing weights' own gradient (the router's) is not computed.
+    The routing weights' own gradient is the router's: mx_combine_dweights of
+    layer.y, as moe_block.MoEBlock takes it.
     Every row of the layer's buffers is a slot (M = T k); entries routed to
     an expert outside [0, G) are dropped."""
 
