@@ -14,7 +14,6 @@ import torch
 
 from . import _check, load
 from .training import _empty as _empty_on
-from .training import _same_device
 
 SIGMOID, RENORM, LOGITS_BF16 = 1, 2, 4
 STREAM_FP32, WEIGHT_FP32 = 1, 2
@@ -52,10 +51,12 @@ def _lib():
     return lib
 
 
-# Small calls are bound by the host's part, so the checks below avoid what
-# costs a microsecond each: stream and device objects (the raw handle is read
-# where this torch has it), tests of what a call has made itself.
+# Small calls are bound by the host's part (a launch is 3 us of it), so the
+# checks below avoid what costs a microsecond: stream and device objects (the
+# raw handles are read where this torch has them), sets and generators, tests
+# of what a call has made itself.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name, at, stream, *args):
@@ -68,14 +69,24 @@ def _call(name, at, stream, *args):
         handle = _raw_stream(at)
     else:
         handle = torch.cuda.current_stream(at).cuda_stream
-    f = getattr(_lib(), name)
-    if at == torch.cuda.current_device():
-        rc = f(*args, handle)
+    if at == _current_device():
+        rc = getattr(_lib(), name)(*args, handle)
     else:
         with torch.cuda.device(at):
-            rc = f(*args, handle)
+            rc = getattr(_lib(), name)(*args, handle)
     if rc:
         _check(rc, name)
+
+
+def _one_gpu(first, *others):
+    """Its number."""
+    at = first.get_device()  # -1: not on a GPU
+    if at < 0:
+        raise ValueError("all tensors must be on one GPU")
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("all tensors must be on one GPU")
+    return at
 
 
 def _empty(rows, columns, dtype, device, stream):
@@ -96,9 +107,10 @@ def _matrix(t, name, dtypes, rows=None, columns=None):
     """The row stride of a matrix (of rows x columns, if given) whose rows are contiguous."""
     if t.dtype not in dtypes:
         raise _wrong_type(t, name, dtypes)
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix")
-    r, c = t.shape
+    r, c = shape
     if rows is not None and (r != rows or c != columns):
         raise ValueError(f"{name} must be a matrix of {rows} x {columns}")
     ld, step = t.stride()
@@ -154,8 +166,8 @@ def mx_router(logits, k, bias=None, groups=1, groups_kept=None, group_top=2, sco
         _whole(scores, "scores", (_FP32,), T, E)
     if bias is not None:
         _whole(bias, "bias", (_FP32,), E)
-    _same_device(logits, bias, experts, weights, scores)
-    _call("mx_router", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, _at(bias), groups,
+    at = _one_gpu(logits, bias, experts, weights, scores)
+    _call("mx_router", at, stream, logits.data_ptr(), ldl, T, E, _at(bias), groups,
           groups if groups_kept is None else groups_kept, group_top, k, scale, flags, experts.data_ptr(),
           weights.data_ptr(), _at(scores))
     return experts, weights, scores
@@ -180,8 +192,8 @@ def mx_router_backward(logits, experts, dweights, dscores=None, score="softmax",
         dlogits = _empty(T, E, logits.dtype, logits.device, stream)
     else:
         ldd = _matrix(dlogits, "dlogits", (logits.dtype,), T, E)
-    _same_device(logits, experts, dweights, dscores, dlogits)
-    _call("mx_router_backward", logits.get_device(), stream, logits.data_ptr(), ldl, T, E, experts.data_ptr(),
+    at = _one_gpu(logits, experts, dweights, dscores, dlogits)
+    _call("mx_router_backward", at, stream, logits.data_ptr(), ldl, T, E, experts.data_ptr(),
           dweights.data_ptr(), _at(dscores), k, scale, flags, dlogits.data_ptr(), ldd)
     return dlogits
 
@@ -199,8 +211,8 @@ def mx_combine_dweights(dout, y, slot_of, dweights=None, stream=None):
         dweights = _empty(T, k, _FP32, dout.device, stream)
     else:
         _whole(dweights, "dweights", (_FP32,), T, k)
-    _same_device(dout, y, slot_of, dweights)
-    _call("mx_combine_dweights", dout.get_device(), stream, dout.data_ptr(), ldd, y.data_ptr(), y.shape[0], ldy,
+    at = _one_gpu(dout, y, slot_of, dweights)
+    _call("mx_combine_dweights", at, stream, dout.data_ptr(), ldd, y.data_ptr(), y.shape[0], ldy,
           slot_of.data_ptr(), T, k, N, dweights.data_ptr())
     return dweights
 
@@ -247,9 +259,9 @@ def mx_rms_norm(x, weight, residual=None, eps=1e-6, h=None, y=True, q=None, s=No
         rstd = _vector(M, _FP32, dev, stream)
     elif rstd is not None:
         _whole(rstd, "rstd", (_FP32,), M)
-    _same_device(x, residual, weight, h, y, q, s, rstd)
+    at = _one_gpu(x, residual, weight, h, y, q, s, rstd)
     flags = (STREAM_FP32 if kind is _FP32 else 0) | (WEIGHT_FP32 if weight.dtype is _FP32 else 0)
-    _call("mx_rms_norm", x.get_device(), stream, x.data_ptr(), ldx, _at(residual), ldr, weight.data_ptr(), M, N, eps,
+    _call("mx_rms_norm", at, stream, x.data_ptr(), ldx, _at(residual), ldr, weight.data_ptr(), M, N, eps,
           flags, _at(h), ldh, _at(y), ldy, _at(q), _at(s), _at(rstd))
     return y, h, q, s, rstd
 
@@ -300,9 +312,9 @@ def mx_rms_norm_backward(dy, h, weight, rstd, dy2=None, dh_in=None, dh=None, dx=
             raise ValueError("workspace must be a contiguous uint8 tensor")
         else:
             size = workspace.numel()
-    _same_device(h, dy, dy2, weight, rstd, dh_in, dh, dx, dweight, workspace)
+    at = _one_gpu(h, dy, dy2, weight, rstd, dh_in, dh, dx, dweight, workspace)
     flags = (STREAM_FP32 if kind is _FP32 else 0) | (WEIGHT_FP32 if weight.dtype is _FP32 else 0)
-    _call("mx_rms_norm_backward", h.get_device(), stream, dy.data_ptr(), ldy, _at(dy2), ldy2, h.data_ptr(), ldh,
+    _call("mx_rms_norm_backward", at, stream, dy.data_ptr(), ldy, _at(dy2), ldy2, h.data_ptr(), ldh,
           weight.data_ptr(), rstd.data_ptr(), _at(dh_in), ldi, M, N, flags, dh.data_ptr(), ldo, _at(dx), lddx,
           _at(dweight), dweight is not None and dweight.dtype is _FP32, bool(accumulate), _at(workspace),
           max(size, 0))
