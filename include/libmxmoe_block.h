@@ -164,9 +164,9 @@ mx_status mx_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *   dweight  NULL, or [N]: bf16 (dw_fp32 = 0) or float32 (dw_fp32 = 1); with
  *            accumulate = 1 the sum is added to the float32 values there
  *            (MX_ERR_UNSUPPORTED for bf16)
- *   workspace  scratch memory of mx_rms_norm_backward_workspace_bytes(M, N),
- *            16-byte aligned, for dweight (MX_ERR_CAPACITY if smaller); calls on
- *            several streams need one each
+ *   workspace  scratch memory of mx_rms_norm_backward_workspace_bytes(M, N)
+ *            (0 for few rows), 16-byte aligned, for dweight (MX_ERR_CAPACITY if
+ *            smaller); calls on several streams need one each
  * dweight is summed in fp32 in an order that depends on the sizes only.
  * M = 0 writes zeros to dweight (with accumulate: no change).  Requirements
  * as above, M < 2^31.  mx_rms_norm_backward_workspace_bytes returns -1 for

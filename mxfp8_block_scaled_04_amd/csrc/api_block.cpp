@@ -142,8 +142,9 @@ mx_status mx_rms_norm_backward(const uint16_t* dy, int64_t ldy, const uint16_t* 
     if (M > 0 && (!dy || !h || !weight || !rstd || !dh)) return MX_ERR_NULL;
     if (M == 0 && (!dweight || accumulate)) return MX_OK;
     if (M > 0 && dweight) {
-        if (workspace_bytes < mx_rms_norm_backward_workspace_bytes(M, N)) return MX_ERR_CAPACITY;
-        if (!workspace) return MX_ERR_NULL;
+        const int64_t needed = mx_rms_norm_backward_workspace_bytes(M, N);
+        if (workspace_bytes < needed) return MX_ERR_CAPACITY;
+        if (needed > 0 && !workspace) return MX_ERR_NULL;
     }
     if (!aligned(dy, 16) || !aligned(dy2, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) ||
         !aligned(dh_in, 16) || !aligned(dh, 16) || !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(workspace, 16))
@@ -155,7 +156,7 @@ mx_status mx_rms_norm_backward(const uint16_t* dy, int64_t ldy, const uint16_t* 
 
 int64_t mx_rms_norm_backward_workspace_bytes(int64_t M, int64_t N) {
     if (check_norm(M, N, 0) != MX_OK) return -1;
-    return 4 * (int64_t)mx::norm_backward_parts(M, N) * N;
+    return mx::norm_backward_needs_parts(M, N) ? 4 * (int64_t)mx::norm_backward_parts(M, N) * N : 0;
 }
 
 }  // extern "C"

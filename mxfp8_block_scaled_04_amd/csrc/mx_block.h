@@ -87,7 +87,8 @@ struct NormBackwardArgs {
     float* workspace;
 };
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
-// Rows of partial sums of dweight that its workspace holds.
+// Rows of partial sums of dweight that its workspace holds, where it is summed from such.
+bool norm_backward_needs_parts(int64_t M, int64_t N);
 int32_t norm_backward_parts(int64_t M, int64_t N);
 
 }  // namespace mx

@@ -14,6 +14,7 @@ hipError_t launch_combine_dweights(const uint16_t*, int64_t, const uint16_t*, in
 }
 hipError_t launch_rms_norm(const NormArgs&, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_rms_norm_backward(const NormBackwardArgs&, hipStream_t) { return hipErrorNotSupported; }
+bool norm_backward_needs_parts(int64_t M, int64_t) { return M > 256; }
 int32_t norm_backward_parts(int64_t M, int64_t) { return M < 4 ? (int32_t)M : 4; }
 
 }  // namespace mx

@@ -130,9 +130,10 @@ def test_norm_backward_refusals():
     # (dy, ldy, dy2, ldy2, h, ldh, weight, rstd, dh_in, ldi, M, N, flags, dh, ldo, dx, lddx, dweight, fp32, accumulate,
     #  workspace, bytes, stream)
     lib = B._lib()
-    size = lib.mx_rms_norm_backward_workspace_bytes(5, 64)
+    M = 5000
+    size = lib.mx_rms_norm_backward_workspace_bytes(M, 64)
     assert size > 0 and size % (4 * 64) == 0
-    f = _variants(lib.mx_rms_norm_backward, (FAKE, 64, FAKE, 64, FAKE, 64, FAKE, FAKE, FAKE, 64, 5, 64, 1, FAKE, 64,
+    f = _variants(lib.mx_rms_norm_backward, (FAKE, 64, FAKE, 64, FAKE, 64, FAKE, FAKE, FAKE, 64, M, 64, 1, FAKE, 64,
                                              FAKE, 64, FAKE, 1, 0, FAKE, size, None))
     assert f(a10=-1) == SHAPE and f(a11=60) == SHAPE and f(a12=4) == SHAPE
     for i in (1, 3, 5, 9, 14, 16):
@@ -154,7 +155,7 @@ def test_norm_backward_refusals():
 def test_norm_workspace():
     f = mx.mx_rms_norm_backward_workspace_bytes
     assert f(-1, 64) == -1 and f(5, 60) == -1 and f(5, 0) == -1 and f(5, 40000) == -1 and f(1 << 31, 64) == -1
-    assert f(0, 64) == 0
+    assert f(0, 64) == 0 and f(1, 64) == 0 and f(100000, 64) > 0
 
 
 def test_the_binding_refuses():

@@ -205,8 +205,8 @@ def test_gradients(kind, N):
     assert alone[2] is None and torch.equal(alone[0], mx.mx_rms_norm_backward(dy, h, weight, rstd)[0])
 
 
-@pytest.mark.parametrize("M", [0, 1, 2, 3, 31, 511, 513, 1025, 5000])
-@pytest.mark.parametrize("N", [64, 520, 2056])
+@pytest.mark.parametrize("M", [0, 1, 2, 3, 31, 511, 256, 257, 513, 1025, 5000])
+@pytest.mark.parametrize("N", [24, 64, 520, 2056])
 def test_weight_gradient_of_every_number_of_rows(N, M):
     gen = torch.Generator().manual_seed(M)
     h, dy = _rows(gen, M, N, "bf16"), _rows(gen, M, N, "bf16")
@@ -248,6 +248,24 @@ def test_gradient_strides_and_in_place(kind, N):
         assert torch.equal(into, want[0])
     got = mx.mx_rms_norm_backward(dy, h, weight, rstd, dy2=dy2, dh_in=dh_in, dh=dh_in)
     assert torch.equal(dh_in, want[0])
+
+
+@pytest.mark.parametrize("M", [200, 256, 3000])
+@pytest.mark.parametrize("N", [128, 1480, 7168])
+def test_gradients_that_replace_dy(N, M):
+    """dweight is that of the dy that was there."""
+    gen = torch.Generator().manual_seed(16)
+    h, dy, dy2 = (_rows(gen, M, N, "bf16") for _ in range(3))
+    weight = torch.randn(N, generator=gen).cuda()
+    rstd = mx.mx_rms_norm(h, weight, eps=EPS, y=None, rstd=True)[4]
+    want = mx.mx_rms_norm_backward(dy, h, weight, rstd, dy2=dy2, dh_in=h, dweight=torch.float32)
+    _check_gradients(want, dy, h, weight, rstd, dy2, h)
+    got = mx.mx_rms_norm_backward(dy, h, weight, rstd, dy2=dy2, dh_in=h, dh=dy, dweight=torch.float32)
+    assert torch.equal(dy, want[0])
+    # the same sum, in the order of the other kernel's workgroups
+    z = (h.double() * rstd.double()[:, None]).abs()
+    size = (z * (dy2.double().abs() + 8)).sum(0)
+    assert ((got[2].double() - want[2].double()).abs() <= size * U * (M / 512 + 512)).all()
 
 
 @pytest.mark.parametrize("N", [16, 640])
