@@ -195,13 +195,13 @@ __device__ __forceinline__ void wave_sync() {
 
 // L: float or uint16_t (bf16).
 template <class L, int W, int ITEMS>
-__global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(RouterArgs g, int32_t lanes_per_group) {
+__global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(RouterArgs g, int32_t lanes_per_group) {
     constexpr int kTeams = kThreads / W;
     constexpr int kList = 2 * W;  // candidates that are ranked
     __shared__ uint64_t list_key[kTeams][kList];
     __shared__ double list_score[kTeams][kList];
     __shared__ int32_t list_expert[kTeams][kList];
-    __shared__ uint64_t chosen_key[kTeams][W];
+    __shared__ uint64_t chosen_key[kTeams][W + 1];
     __shared__ double chosen_score[kTeams][W];
     __shared__ int32_t chosen_expert[kTeams][W];
     const int lane = threadIdx.x & 63;
@@ -233,10 +233,54 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
     // the same in all lanes: no logit of the wave is -infinity, or so far off that its exponential has to be cut
     const bool plain = __ballot(!(sigmoid ? least_logit > -100.0f && top < 100.0f : least_logit - top > -100.0f)) == 0;
 
-    // the softmax's sum: in binary64 where choices need it
+    // scores in binary32
+    float c[ITEMS];
+    float over = 1.0f;  // 1 / the softmax's sum
     double sum = 1.0;
-    float c[ITEMS];  // (here: exponentials)
-    if (!sigmoid && !by_logit) {
+    if (!by_logit || g.scores != nullptr || (!sigmoid && !renorm)) {
+        if (sigmoid) {
+            if (plain) {
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) c[j] = sigmoid_near(l[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) c[j] = sigmoid_of(l[j]);
+            }
+        } else {
+            float part = 0.0f;
+            if (plain) {
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) part += c[j] = exp_of(l[j] - top);
+            } else {
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) part += c[j] = l[j] == kLowest ? 0.0f : exp_below(l[j] - top);
+            }
+            part = team_sum<W>(part);
+            sum = (double)part;
+            over = part == 0.0f ? 0.0f : 1.0f / part;
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) c[j] *= over;
+        }
+        if (g.scores != nullptr) store_values<ITEMS>(g.scores + token * g.E + base, here, c);
+    }
+    // (of finite logits, or NaN)
+    const auto score64 = [&](float v) {
+        return sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / sum;
+    };
+    const auto choice64 = [&](int32_t expert, double* score) {  // as a key; 0: cannot be chosen
+        const float v = load_logit(row + expert), b = g.bias != nullptr ? g.bias[expert] : 0.0f;
+        const double s = score64(v);
+        *score = s;
+        return v == kLowest || b == kLowest ? 0 : key_of(by_logit ? (double)v + 0.0 : s + (double)b);
+    };
+    // The softmax's sum above is of binary32, ITEMS terms in a row, 6 joins and 8 half steps of a term off at most (here:
+    // twice that): choices that are no more than that part of the largest score apart are formed again with one of binary64
+    // (a pair in thousands; all of them: 512 experts, 16384 tokens 29 us, now 15).
+    constexpr float kSumError = (ITEMS + 14) * 0x1p-23f;
+    bool exact = sigmoid || by_logit;
+    const auto sum_exactly = [&]() {
+        if (exact) return;
+        exact = true;
         sum = 0.0;
 #pragma unroll 2
         for (int j = 0; j < here; ++j) {  // (read again: registers have no index)
@@ -244,38 +288,6 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
             if (v != kLowest) sum += exp((double)v - (double)top);
         }
         sum = team_reduce<W>(sum, [](double p, double q) { return p + q; });
-    } else if (!sigmoid && (!renorm || g.scores != nullptr)) {
-        float part = 0.0f;
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) part += c[j] = l[j] == kLowest ? 0.0f : exp_below(l[j] - top);
-        part = team_sum<W>(part);
-        sum = (double)part;
-        if (g.scores != nullptr) {
-            const float over = part == 0.0f ? 0.0f : 1.0f / part;
-#pragma unroll
-            for (int j = 0; j < ITEMS; ++j) c[j] *= over;
-            store_values<ITEMS>(g.scores + token * g.E + base, here, c);
-        }
-    }
-    const float over = (float)(1.0 / sum);
-    const auto score32 = [&](float v) {
-        if (v == kLowest) return 0.0f;
-        return sigmoid ? sigmoid_of(v) : exp_below(v - top) * over;
-    };
-    // (of finite logits, or NaN)
-    const auto score64 = [&](float v) {
-        return sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / sum;
-    };
-    if (g.scores != nullptr && (sigmoid || !by_logit)) {
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) c[j] = score32(l[j]);
-        store_values<ITEMS>(g.scores + token * g.E + base, here, c);
-    }
-    const auto choice64 = [&](int32_t expert, double* score) {  // as a key; 0: cannot be chosen
-        const float v = load_logit(row + expert), b = g.bias != nullptr ? g.bias[expert] : 0.0f;
-        const double s = score64(v);
-        *score = s;
-        return v == kLowest || b == kLowest ? 0 : key_of(by_logit ? (double)v + 0.0 : s + (double)b);
     };
 
     // choices in binary32: -infinity what cannot be chosen, +infinity also for NaN
@@ -284,27 +296,21 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
         for (int j = 0; j < ITEMS; ++j) c[j] = fminf(l[j], -kLowest);
     } else {
         if (g.bias != nullptr) {
-            load_logits<ITEMS>(g.bias + base, here, c);
-        } else {
+            float b[ITEMS];
+            load_logits<ITEMS>(g.bias + base, here, b);
 #pragma unroll
-            for (int j = 0; j < ITEMS; ++j) c[j] = 0.0f;
+            for (int j = 0; j < ITEMS; ++j) c[j] += b[j];
         }
-        if (plain && sigmoid) {
 #pragma unroll
-            for (int j = 0; j < ITEMS; ++j) c[j] = fminf(c[j] + sigmoid_near(l[j]), -kLowest);
-        } else if (plain) {
+        for (int j = 0; j < ITEMS; ++j) c[j] = fminf(c[j], -kLowest);
+        if (!plain) {
 #pragma unroll
-            for (int j = 0; j < ITEMS; ++j) c[j] = fminf(c[j] + exp_of(l[j] - top) * over, -kLowest);
-        } else {
-#pragma unroll
-            for (int j = 0; j < ITEMS; ++j) {
-                c[j] = l[j] == kLowest ? kLowest : fminf(c[j] + score32(l[j]), -kLowest);
-            }
+            for (int j = 0; j < ITEMS; ++j) c[j] = l[j] == kLowest ? kLowest : c[j];
         }
     }
-    // a score is within this of its true value: 2^-19 of the largest one (rounding of l - max, 3 steps of the exponential,
-    // 2 of the quotient; |x| e^x < 0.4), or it has underflowed
-    const float off = by_logit ? 0.0f : 0x1p-19f * (sigmoid ? score32(top) : over) + 0x1p-120f;
+    // a score is within this of its true value: 2^-19 of the largest one (rounding of l - max, 3 steps of the exponential, 2
+    // of the quotient; |x| e^x < 0.4) and the sum's error, or it has underflowed
+    const float off = by_logit ? 0.0f : (sigmoid ? 0x1p-19f * sigmoid_of(top) : (0x1p-19f + kSumError) * over) + 0x1p-120f;
 
     if (g.groups > 1) {
         Top2 t{kLowest, kLowest};
@@ -338,6 +344,7 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
             undecided = next != kLowest && !(last - next > 4.0f * tau);
         }
         if (__ballot(undecided) != 0) {
+            sum_exactly();
             const float from = fmaxf((g.top > 1 ? t.b : t.a) - 2.0f * tau, -__FLT_MAX__);  // (of NaN: the lowest)
             uint64_t some = 0;
 #pragma unroll
@@ -400,22 +407,29 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
         }
     }
 
-    // candidates, in the order of their indices (the lowest in the highest bit)
-    uint64_t mask = 0;
+    // candidates, in the order of their indices
+    int count = 0;
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        if constexpr (ITEMS <= 32) mask = (uint32_t)mask + (uint32_t)mask + (c[j] >= least);
-        else mask = mask + mask + (c[j] >= least);
-    }
-    const int count = ITEMS <= 32 ? __popc((uint32_t)mask) : __popcll(mask);
+    for (int j = 0; j < ITEMS; ++j) count += c[j] >= least;
     int place = team_scan<W>(count, a);
     const int candidates = __shfl(place, W - 1, W);
     place -= count;
+    uint64_t mask = 0;  // those that are not in the list yet, the first one in the highest bit
+    if (__ballot(candidates > kList) == 0) {
+        int32_t* entry = &list_expert[team][place];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+            if (c[j] >= least) *entry++ = base + j;
+    } else {
+        sum_exactly();
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) mask |= c[j] >= least ? 1ull << (ITEMS - 1 - j) : 0;
+    }
 
     int taken = 0, held = 0;  // candidates that were in the list, entries that stay in it
     while (true) {
         while (mask != 0 && place - taken + held < kList) {
-            const int high = ITEMS <= 32 ? 31 - __clz((uint32_t)mask) : 63 - __clzll(mask);
+            const int high = 63 - __clzll(mask);
             mask ^= 1ull << high;
             list_expert[team][place++ - taken + held] = base + ITEMS - 1 - high;
         }
@@ -426,6 +440,8 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
             const int at = p * W + a;
             if (at >= held && at < entries)
                 list_key[team][at] = choice64(list_expert[team][at], &list_score[team][at]);
+            else if (at >= entries)
+                list_key[team][at] = 0;
         }
         wave_sync();
         // among equal ones the lower place is the lower index: what stayed comes first
@@ -433,10 +449,15 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
             const int at = p * W + a;
             const uint64_t mine = at < entries ? list_key[team][at] : 0;
             int rank = 0;
-            for (int i = 0; i < entries; ++i) {
-                const uint64_t other = list_key[team][i];
-                rank += i < at ? other >= mine : other > mine;
+            for (int i = 0; i < entries; i += 4) {  // (kList is a multiple; what is behind the entries does not count)
+                uint64_t other[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) other[u] = list_key[team][i + u];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    rank += other[u] > mine || (other[u] == mine && i + u < at);
             }
+            if (at < entries && rank == g.k) chosen_key[team][rank] = mine;
             if (at < entries && rank < g.k) {
                 chosen_key[team][rank] = mine;
                 chosen_expert[team][rank] = mine != 0 ? list_expert[team][at] : -1;
@@ -444,6 +465,14 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 8 : 1) void router_kernel(R
             }
         }
         wave_sync();
+        if (!exact) {  // (then all candidates are in the list)
+            const bool close = a < g.k && a + 1 < entries &&
+                               !(value_of(chosen_key[team][a]) - value_of(chosen_key[team][a + 1]) > (double)(kSumError * over));
+            if (__ballot(close) != 0) {
+                sum_exactly();
+                continue;
+            }
+        }
         taken += entries - held;
         held = entries < g.k ? entries : g.k;
         if (__ballot(taken < candidates) == 0) break;
@@ -502,7 +531,7 @@ hipError_t pick_team(const RouterArgs& g, hipStream_t stream) {
         while (W < 64 && (W < choices || W < padded || size > items * (W / padded))) W *= 2;
         return W;
     };
-    // A narrow team has less work per token (32768 tokens, 256 experts: 64 lanes 46 us, 32 27, 16 23) but a longer way
+    // A narrow team has less work per token (32768 tokens, 256 experts: 64 lanes 46 us, 32 27, 16 21) but a longer way
     // through it (1024 tokens: 6.9, 7.0, 9.9): taken where the waves fill the 1024 vector units once, or twice, and
     // where its list has room for 4 k candidates.
     int W = team(4, g.k);

@@ -177,6 +177,22 @@ def test_choices_that_float32_cannot_tell_apart(score):
         _check(l.cuda(), 8, score=score, bias=bias, groups=4, groups_kept=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,step", [(32, 8, 2.0 ** -23), (64, 6, 2.0 ** -21), (256, 8, 2.0 ** -22), (256, 8, 2.0 ** -18),
+                                      (1024, 16, 2.0 ** -20)])
+def test_choices_a_few_float32_steps_apart(E, k, step, score):
+    """The bias cancels the first row's scores and orders its experts by steps
+    that are near what sums in float32 are off."""
+    for seed in range(6):
+        gen = torch.Generator().manual_seed(seed)
+        l = torch.randn((300, E), generator=gen) * 2
+        s = torch.from_numpy(_scores(l.double().numpy(), score))
+        bias = (0.25 - s[0] + step * torch.randperm(E, generator=gen)).float().cuda()
+        l[1:150] = l[0]
+        for groups in (1, 4):
+            _check(l.cuda(), k, score=score, bias=bias, groups=groups, groups_kept=max(1, groups // 2))
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
