@@ -101,8 +101,8 @@ mx_status mx_router_backward(const void* logits, int64_t ldl, int64_t T, int32_t
  *   dweights float32 [T][k] out
  * Requires N % 8 == 0 (MX_ERR_UNSUPPORTED), ldd, ldy >= N, k >= 1
  * (MX_ERR_SHAPE), dout, y 16-byte aligned, ldd, ldy % 8 == 0, slot_of and
- * dweights 4-byte aligned (MX_ERR_ALIGN); T < 2^24 and T k < 2^31
- * (MX_ERR_UNSUPPORTED).
+ * dweights 4-byte aligned (MX_ERR_ALIGN); T < 2^24, M and T k < 2^31, ldd and
+ * ldy < 2^30 (MX_ERR_UNSUPPORTED).
  */
 mx_status mx_combine_dweights(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t M, int64_t ldy,
                               const int32_t* slot_of, int64_t T, int32_t k, int64_t N, float* dweights, void* stream);
@@ -140,8 +140,8 @@ enum {
  * (MX_ERR_UNSUPPORTED).  Requires N % 8 == 0, N > 0, strides >= N, eps >= 0 and
  * finite (MX_ERR_SHAPE; with eps = 0 a row of zeros gives NaN, as the formula
  * has it), 16-byte aligned pointers (rstd, s: 4), strides that are multiples
- * of 8 (MX_ERR_ALIGN).  Rows that are not finite give y as the formula
- * does and unspecified codes.
+ * of 8 (MX_ERR_ALIGN) and below 2^30 (MX_ERR_UNSUPPORTED).  Rows that are not
+ * finite give y as the formula does and unspecified codes.
  */
 mx_status mx_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, int64_t M,
                       int64_t N, float eps, uint32_t flags, void* h, int64_t ldh, uint16_t* y, int64_t ldy,

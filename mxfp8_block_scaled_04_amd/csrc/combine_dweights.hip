@@ -4,6 +4,9 @@
 // dout in registers and takes the token's rows 8 entries at a time (their
 // loads in flight together), one fp32 sum per entry; the sums are joined over
 // the lanes of a wave in registers and over the waves through LDS.
+// What bounds it: HBM.  Measured: 4096 tokens, k = 8, 7168 columns 77 us, 6.8
+// TB/s (each row of y read once, each of dout once per 8 entries); 509 tokens,
+// k = 3, 1480 columns 3.8.
 #include "mx_bf16.h"
 #include "mx_block.h"
 #include "mx_device.h"

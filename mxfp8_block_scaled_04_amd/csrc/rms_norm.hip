@@ -11,8 +11,8 @@
 // is read and written once; the sum over the row is a reduction in registers
 // and, where a workgroup is the team, LDS.  Measured on 32768 rows of 7168,
 // bf16: forward with residual and MXFP8 rows (9.03 bytes an element)
-// 353 us, 6.0 TB/s; backward with both output gradients and the
-// stream's (10 bytes) 415 us, 5.7 TB/s; a copy reaches 5.1
+// 351 us, 6.05 TB/s; backward with both output gradients and the
+// stream's (10 bytes) 414 us, 5.7 TB/s; a copy reaches 5.1
 // TB/s, the 2:1 stream of mx_stream21 6.6.
 //
 // Teams: a wave, half, a quarter or an eighth of one for rows of up to 1024,
@@ -52,18 +52,22 @@ using Raw = typename std::conditional<sizeof(S) == 2, uint4, Eight>::type;
 __device__ __forceinline__ Eight values(uint4 d) { return unpack(d); }
 __device__ __forceinline__ const Eight& values(const Eight& e) { return e; }
 
-// Rows are read once: non-temporal loads (forward as above 410 -> 370 us).
-// Not of float32, where an instruction takes every other 16 bytes: the second
-// one finds its lines in the cache then (8192 columns, residual in float32: 303
-// -> 287 us; the stores as well, 505 -> 303).
-__device__ __forceinline__ uint4 load_raw(const uint16_t* p) { return load_stream16(p); }
-__device__ __forceinline__ Eight load_raw(const float* p) {
+// Rows are read once: `far`, by non-temporal loads (forward as above 410 ->
+// 370 us), in calls that are large enough to pass the caches (below); in others
+// they may still be there (forward, 2048 rows of 7168 in turn with two others: 26 us
+// with them, 21.5 without).  Not of float32, where an instruction takes every
+// other 16 bytes: the second one finds its lines in the cache then (8192
+// columns, residual in float32: 303 -> 287 us; the stores as well, 505 -> 303).
+__device__ __forceinline__ uint4 load_raw(const uint16_t* p, bool far) {
+    return far ? load_stream16(p) : *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ Eight load_raw(const float* p, bool) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     return Eight{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 // The weight is read for every row.
 __device__ __forceinline__ Eight load_kept(const uint16_t* p) { return unpack(*reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ Eight load_kept(const float* p) { return load_raw(p); }
+__device__ __forceinline__ Eight load_kept(const float* p) { return load_raw(p, false); }
 
 // Outputs of large calls leave the caches before anything reads them: from
 // 2^25 elements on, where a call's rows pass the 256 MB of the Infinity Cache,
@@ -147,13 +151,13 @@ __global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void rms
             h[v] = Eight{};
             if (live && c < N) {
                 if (g.residual != nullptr) {
-                    h[v] = unpack(load_raw((const uint16_t*)g.x + row * g.ldx + c));
-                    const Eight r = values(load_raw((const S*)g.residual + row * g.ldr + c));
+                    h[v] = unpack(load_raw((const uint16_t*)g.x + row * g.ldx + c, far));
+                    const Eight r = values(load_raw((const S*)g.residual + row * g.ldr + c, far));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) h[v].v[i] += r.v[i];
                     store_row((S*)g.h + row * g.ldh + c, h[v], far);
                 } else {
-                    h[v] = values(load_raw((const S*)g.x + row * g.ldx + c));
+                    h[v] = values(load_raw((const S*)g.x + row * g.ldx + c, far));
                 }
             }
 #pragma unroll
@@ -246,7 +250,7 @@ struct Row {
     uint4 dy[V], dy2[V];
     Raw<S> h[V], in[AHEAD ? V : 1];
     float r;
-    __device__ __forceinline__ void load(const NormBackwardArgs& g, int64_t row, int first, int step) {
+    __device__ __forceinline__ void load(const NormBackwardArgs& g, int64_t row, int first, int step, bool far) {
         const bool live = row < g.M;
         r = live ? g.rstd[row] : 0.0f;
 #pragma unroll
@@ -256,11 +260,11 @@ struct Row {
             h[v] = Raw<S>{};
             if constexpr (AHEAD) in[v] = Raw<S>{};
             if (!live || c >= g.N) continue;
-            h[v] = load_raw((const S*)g.h + row * g.ldh + c);
-            dy[v] = load_raw(g.dy + row * g.ldy + c);
-            if (g.dy2 != nullptr) dy2[v] = load_raw(g.dy2 + row * g.ldy2 + c);
+            h[v] = load_raw((const S*)g.h + row * g.ldh + c, far);
+            dy[v] = load_raw(g.dy + row * g.ldy + c, far);
+            if (g.dy2 != nullptr) dy2[v] = load_raw(g.dy2 + row * g.ldy2 + c, far);
             if constexpr (AHEAD)
-                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c);
+                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c, far);
         }
     }
     // z, and g in e
@@ -295,7 +299,7 @@ __device__ __forceinline__ void dweight_slice(const NormBackwardArgs& g, int64_t
 #pragma unroll 4
     for (int64_t row = threadIdx.x >> 2; row < g.M; row += blockDim.x >> 2) {
         Row<S, 1, false> x;
-        x.load(g, row, c, 0);
+        x.load(g, row, c, 0, false);
         Eight z, e;
         x.take(g, 0, z, e);
 #pragma unroll
@@ -350,13 +354,13 @@ __global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void nor
     const int64_t stride = blocks * kTeams;
     int64_t row = block * kTeams + mine;
     Row<S, V, AHEAD> x;
-    if constexpr (AHEAD) x.load(g, row, first, step);
+    if constexpr (AHEAD) x.load(g, row, first, step, far);
     int turn = 0;
     for (int64_t r0 = block * kTeams; r0 < g.M; r0 += stride, row += stride, turn ^= 1) {
         Eight z[V], e[V];
         Raw<S> in[V];
         float sum = 0.0f;
-        if constexpr (!AHEAD) x.load(g, row, first, step);
+        if constexpr (!AHEAD) x.load(g, row, first, step, far);
         const float r = x.r;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -372,7 +376,7 @@ __global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void nor
                 sum = __builtin_fmaf(e[v].v[i], z[v].v[i], sum);
             }
         }
-        if constexpr (AHEAD) x.load(g, row + stride, first, step);
+        if constexpr (AHEAD) x.load(g, row + stride, first, step, far);
         const float mean = row_sum<LANES>(sum, buffer[turn]) / (float)N;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -380,7 +384,7 @@ __global__ __launch_bounds__(LANES > 0 ? kTeamThreads : 64 * kMaxWaves) void nor
             if (row >= g.M || c >= N) continue;
             if constexpr (!AHEAD) {
                 in[v] = Raw<S>{};
-                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c);
+                if (g.dh_in != nullptr) in[v] = load_raw((const S*)g.dh_in + row * g.ldi + c, far);
             }
             const Eight from = values(in[v]);
             Eight out;
@@ -428,7 +432,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_long_kernel(Norm
 #pragma unroll 2
         for (int c = first; c < N; c += step) {
             Row<S, 1, false> x;
-            x.load(g, row, c, 0);
+            x.load(g, row, c, 0, far);
             Eight z, e;
             x.take(g, 0, z, e);
             const Eight w = load_kept((const WT*)g.weight + c);
@@ -445,7 +449,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_long_kernel(Norm
 #pragma unroll 2
         for (int c = first; c < N; c += step) {
             Row<S, 1, true> x;
-            x.load(g, row, c, 0);
+            x.load(g, row, c, 0, far);
             Eight z, e;
             x.take(g, 0, z, e);
             const Eight w = load_kept((const WT*)g.weight + c), from = values(x.in[0]);

@@ -20,6 +20,13 @@
 // far as it goes, and its k best stay in it for the next ones.  Group scores
 // that binary32 cannot tell apart are formed again from the few largest
 // choices of each group in binary64.
+//
+// What bounds it: vector instructions, about 260 per token at 256 experts and
+// k = 8 (HBM would take 7 us for what follows).  Measured: 32768 tokens to 8 of
+// 256 experts in 8 groups, sigmoid, bias, float32 logits 20 us; 8191 tokens to
+// 6 of 165 in 3 groups, softmax, all scores written, bf16 9.9; 16 tokens 6.4,
+// the chain of reductions.  k rounds of "the largest that is left" in binary64
+// took 59, 18 and 7.6.
 #include <type_traits>
 
 #include "mx_bf16.h"
@@ -555,7 +562,11 @@ hipError_t pick_team(const RouterArgs& g, hipStream_t stream) {
 //   dl_e = s_e (ds_e - sum_f s_f ds_f), or s_e (1 - s_e) ds_e.
 // A team of W lanes has a token: lane i < k its choice i, and each lane 8
 // consecutive experts of every 8 W, which it stores in one piece.  The choices'
-// parts find their experts through a row in LDS.
+// parts find their experts through a row in LDS (comparing every expert with
+// every choice took 32 us for the first of what follows).
+// What bounds it: the latency of the gathered logits, and a launch.  Measured:
+// 32768 tokens, 8 of 256 experts, sigmoid, renormalised, bf16 8 us (2.2 TB/s
+// written); 4096 tokens, 8 of 128, softmax with a gradient of the scores 5.0.
 // ---------------------------------------------------------------------------
 
 // s(v) and 1 - s(v) of the sigmoid, each with its own relative precision.
