@@ -62,7 +62,7 @@ enum {
  * groups == 0, 1 <= groups_kept <= groups, k <= groups_kept E / groups,
  * group_top 1 or 2, ldl >= E, finite scale (MX_ERR_SHAPE); pointers aligned to
  * their elements (MX_ERR_ALIGN); T < 2^24, and for a number of groups that is
- * no power of two E p / groups <= 4096 with p the next one
+ * no power of two E p / groups <= 4096 with p the next one; strides < 2^32
  * (MX_ERR_UNSUPPORTED).
  */
 mx_status mx_router(const void* logits, int64_t ldl, int64_t T, int32_t E, const float* bias, int32_t groups,
@@ -157,10 +157,11 @@ mx_status mx_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *   h        [M][ldh] of the stream's type; rstd float32 [M]
  *   dh_in    NULL, or [M][ldi] of the stream's type: the gradient that reaches
  *            h from behind (the residual stream)
- *   dh       [M][ldo] of the stream's type, out; it may be dh_in or, for a
- *            bf16 stream, dy (same stride)
+ *   dh       [M][ldo] of the stream's type, out
  *   dx       NULL, or bf16 [M][lddx] out: the value of dh rounded to bf16 (only
  *            for a float32 stream, MX_ERR_SHAPE: of a bf16 one dh is it)
+ *            dh and dx may each be one of dy, dy2, h and dh_in, where type and
+ *            stride are the same; outputs overlap nothing else
  *   dweight  NULL, or [N]: bf16 (dw_fp32 = 0) or float32 (dw_fp32 = 1); with
  *            accumulate = 1 the sum is added to the float32 values there
  *            (MX_ERR_UNSUPPORTED for bf16)

@@ -17,13 +17,13 @@ mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; 
 constexpr int32_t kMaxExperts = 4096;
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;  // a team of up to 64 lanes each: the grid's limit
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // a row's offset in bytes stays far below 2^63
+constexpr int64_t kMaxStride = (int64_t)1 << 32;  // of a token: offsets in bytes stay far below 2^63
 
 mx_status check_router(int64_t ldl, int64_t T, int32_t E, int32_t k, float scale, uint32_t flags) {
     if (T < 0 || E < 1 || E > kMaxExperts || k < 1 || k > MX_ROUTER_MAX_K || ldl < E || !std::isfinite(scale))
         return MX_ERR_SHAPE;
     if ((flags & ~(uint32_t)(MX_ROUTER_SIGMOID | MX_ROUTER_RENORM | MX_ROUTER_LOGITS_BF16)) != 0) return MX_ERR_SHAPE;
-    if (T >= kMaxTokens || ldl >= kMaxStride / 4) return MX_ERR_UNSUPPORTED;
+    if (T >= kMaxTokens || ldl >= kMaxStride) return MX_ERR_UNSUPPORTED;
     return MX_OK;
 }
 
@@ -74,7 +74,7 @@ mx_status mx_router_backward(const void* logits, int64_t ldl, int64_t T, int32_t
     const mx_status st = check_router(ldl, T, E, k, scale, flags);
     if (st == MX_ERR_SHAPE || k > E || ldd < E) return MX_ERR_SHAPE;
     if (st != MX_OK) return st;
-    if (ldd >= kMaxStride / 4) return MX_ERR_UNSUPPORTED;
+    if (ldd >= kMaxStride) return MX_ERR_UNSUPPORTED;
     if (T == 0) return MX_OK;
     if (!logits || !experts || !dweights || !dlogits) return MX_ERR_NULL;
     const size_t size = flags & MX_ROUTER_LOGITS_BF16 ? 2 : 4;

@@ -502,7 +502,8 @@ constexpr int64_t kBackwardOne = 64 * kMaxWaves;  // rows of up to so many vecto
 // Up to so many rows (of up to 16384 columns) dweight is computed from the rows
 // again, which are in the caches, instead of from parts: one launch for all of
 // it and no workspace (64 rows of 7168 7.6 -> 5.9
-// us and 3 us less on the host; 1531 of 1480 would take 27 against 11).  Where dh replaces dy, it is computed before.
+// us and 3 us less on the host; 1531 of 1480 would take 27 against 11).  Where an output
+// replaces an input, it is computed before.
 constexpr int64_t kFewRows = 256;
 bool few_rows(int64_t M, int64_t N) { return M > 0 && M <= kFewRows && N <= 16 * 64 * kMaxWaves; }
 
@@ -522,7 +523,10 @@ hipError_t run_backward(const NormBackwardArgs& g, hipStream_t stream) {
     const bool few = g.dweight != nullptr && few_rows(g.M, g.N);
     const int32_t columns = (int32_t)((g.N + kSlice - 1) / kSlice);
     int32_t slices = few ? columns : 0;
-    if (few && (const void*)g.dh == (const void*)g.dy) {
+    const auto replaces = [&](const void* out) {  // what dweight is computed from
+        return out != nullptr && (out == (const void*)g.dy || out == (const void*)g.dy2 || out == g.h);
+    };
+    if (few && (replaces(g.dh) || replaces(g.dx))) {
         hipLaunchKernelGGL((norm_slices_kernel<S>), dim3(columns), dim3(64 * kMaxWaves), 0, stream, g);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

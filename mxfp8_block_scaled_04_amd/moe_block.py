@@ -68,6 +68,8 @@ class MoEBlock:
 
     def __init__(self, T, k, E, H, I, device="cuda", score="softmax", renorm=True, scale=1.0, groups=1,
                  groups_kept=None, group_top=2, eps=1e-6, stream_dtype=torch.bfloat16):
+        if E % 8:
+            raise ValueError("the number of experts must be a multiple of 8 (of the gate's product)")
         self.T, self.k, self.E, self.H, self.I = T, k, E, H, I
         self.routed = RoutedMoELayer(T, k, E, H, I, device)
         self.norm = _Norm(T, H, eps, stream_dtype, device)

@@ -60,7 +60,7 @@ def test_router_refusals():
     assert f(a8=0) == SHAPE and f(a8=65, a5=1, a6=1, a3=128, a1=128) == SHAPE
     assert f(a8=33) == SHAPE  # more than the experts of the groups kept
     assert f(a9=float("nan")) == SHAPE and f(a9=float("inf")) == SHAPE and f(a10=8) == SHAPE
-    assert f(a2=1 << 24) == UNSUPPORTED
+    assert f(a2=1 << 24) == UNSUPPORTED and f(a1=1 << 32) == UNSUPPORTED
     assert f(a2=0, a3=3000, a1=3000, a5=60, a6=60) == OK  # 50 experts in each of 64 group places
     assert f(a3=4092, a1=4092, a5=33, a6=33) == UNSUPPORTED  # 124 experts in each of 64 group places
     for i in (0, 11, 12):
@@ -78,7 +78,7 @@ def test_router_backward_refusals():
     assert f(a1=63) == SHAPE and f(a11=63) == SHAPE and f(a2=-1) == SHAPE and f(a3=0) == SHAPE
     assert f(a7=0) == SHAPE and f(a7=65, a3=128, a1=128, a11=128) == SHAPE and f(a7=5, a3=4) == SHAPE
     assert f(a8=float("nan")) == SHAPE and f(a9=8) == SHAPE
-    assert f(a2=1 << 24) == UNSUPPORTED
+    assert f(a2=1 << 24) == UNSUPPORTED and f(a1=1 << 32) == UNSUPPORTED and f(a11=1 << 32) == UNSUPPORTED
     for i in (0, 4, 5, 10):
         assert f(**{f"a{i}": None}) == NULL
         assert f(**{f"a{i}": P(0x100002)}) == ALIGN

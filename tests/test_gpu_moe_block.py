@@ -146,6 +146,11 @@ def test_without_a_residual_the_input_is_the_stream():
         block.forward(t["x"], None, t["norm"], t["gate"])
 
 
+def test_the_number_of_experts_is_checked():
+    with pytest.raises(ValueError, match="multiple of 8"):
+        MoEBlock(T, K, 12, H, I)
+
+
 def test_two_blocks_captured_and_replayed():
     """A dense and a routed block one after the other, forward and backward."""
     t, u = _tensors(5, experts=1), _tensors(6)
