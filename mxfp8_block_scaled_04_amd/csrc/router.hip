@@ -158,8 +158,10 @@ struct Top2 {
         b = __builtin_amdgcn_fmed3f(a, b, v);
         a = fmaxf(a, v);
     }
-    // the group's score: the sum of both, or of the one that is there
-    __device__ __forceinline__ float score(int top) const { return top > 1 && b != kLowest ? a + b : a; }
+    // the group's score: the sum of both (finite, as a group without any has -infinity), or of the one that is there
+    __device__ __forceinline__ float score(int top) const {
+        return top > 1 && b != kLowest ? fmaxf(a + b, -__FLT_MAX__) : a;
+    }
 };
 struct Keys2 {
     uint64_t a, b;

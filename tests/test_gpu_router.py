@@ -220,6 +220,26 @@ def test_masks(groups, kept, renorm, score, kind):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,kept,k", [(1, 1, 12), (8, 3, 9), (8, 7, 16), (4, 4, 16)])
+def test_biases_of_the_lowest_value(groups, kept, k, score):
+    """Experts held back by the lowest finite value come after all others and before
+    those that -infinity takes out, in the order of their indices."""
+    E = 64
+    lowest = torch.finfo(torch.float32).min
+    gen = torch.Generator().manual_seed(19)
+    for seed in range(8):
+        l = _logits(20, E, "fp32", 100 + seed)
+        bias = torch.zeros(E)
+        bias[torch.rand(E, generator=gen) < 0.8] = lowest
+        bias[torch.rand(E, generator=gen) < 0.3] = -math.inf
+        if seed % 2:  # whole groups of each kind
+            bias[:16], bias[16:40] = -math.inf, lowest
+        _check(l, k, score=score, bias=bias.cuda(), groups=groups, groups_kept=kept)
+        l[:, bias == lowest] = lowest
+        _check(l, k, score=score, groups=groups, groups_kept=kept, group_top=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_nan_and_infinities(with_bias, score):
     l = _logits(6, 16, "fp32", 13)
