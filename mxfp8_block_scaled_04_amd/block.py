@@ -303,6 +303,8 @@ def mx_rms_norm_backward(dy, h, weight, rstd, dy2=None, dh_in=None, dh=None, dx=
         raise ValueError("accumulate needs dweight")
     elif dweight is not None:
         dweight = _vector(N, weight.dtype if dweight is True else dweight, dev, stream)
+        if dweight.dtype is not _FP32 and dweight.dtype is not _BF16:
+            raise _wrong_type(dweight, "dweight", (_BF16, _FP32))
     if dweight is not None:
         if workspace is None:
             size = _lib().mx_rms_norm_backward_workspace_bytes(M, N)

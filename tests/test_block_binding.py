@@ -84,3 +84,15 @@ def test_the_current_gpu_is_not_set_again(calls, monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", None)
     _all()
     assert [c[0] for c in calls] == NAMES
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int32, torch.uint8])
+def test_dweight_has_a_type_that_the_kernels_write(calls, dtype):
+    x, w, r = torch.zeros(3, 8, dtype=torch.bfloat16), torch.zeros(8), torch.zeros(3)
+    with pytest.raises(TypeError, match="dweight must be bfloat16 or float32"):
+        B.mx_rms_norm_backward(x, x, w, r, dweight=dtype)
+    with pytest.raises(TypeError, match="dweight must be bfloat16 or float32"):
+        B.mx_rms_norm_backward(x, x, w, r, dweight=torch.zeros(8).to(dtype))
+    assert calls == []
+    for d in (torch.bfloat16, torch.float32):
+        assert B.mx_rms_norm_backward(x, x, w, r, dweight=d)[2].dtype is d
