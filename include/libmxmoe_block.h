@@ -168,7 +168,8 @@ mx_status mx_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *   workspace  scratch memory of mx_rms_norm_backward_workspace_bytes(M, N)
  *            (0 for few rows), 16-byte aligned, for dweight (MX_ERR_CAPACITY if
  *            smaller); calls on several streams need one each
- * dweight is summed in fp32 in an order that depends on the sizes only.
+ * dweight is summed in fp32 in an order that depends only on the sizes and, for
+ * few rows, on whether an output replaces dy, dy2 or h.
  * M = 0 writes zeros to dweight (with accumulate: no change).  Requirements
  * as above, M < 2^31.  mx_rms_norm_backward_workspace_bytes returns -1 for
  * sizes that the call refuses.

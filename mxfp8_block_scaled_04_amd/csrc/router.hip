@@ -369,11 +369,11 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
                 u.b = u.b > ob ? u.b : ob;
                 u.add(oa);
             }
-            const uint64_t exact = u.score(g.top);
+            const uint64_t score = u.score(g.top);
             ahead = 0;
             for (int h = 0; h < g.groups; ++h) {
-                const uint64_t other = __shfl((unsigned long long)exact, h * lanes_per_group, W);
-                ahead += other > exact || (other == exact && h < group);
+                const uint64_t other = __shfl((unsigned long long)score, h * lanes_per_group, W);
+                ahead += other > score || (other == score && h < group);
             }
         }
         if (ahead >= g.kept)
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
     // threshold
     float least = -__FLT_MAX__;
     if constexpr (W * ITEMS > kList) {
-        constexpr int kBlocks = ITEMS < 2 ? 1 : ITEMS <= 16 ? 2 : ITEMS / 8;
+        constexpr int kBlocks = ITEMS <= 16 ? 2 : ITEMS / 8;
         uint32_t block[kBlocks];
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
