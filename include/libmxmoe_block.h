@@ -78,8 +78,12 @@ mx_status mx_router(const void* logits, int64_t ldl, int64_t T, int32_t E, const
  *           RENORM (0 where S is 0), and of scale g[i] without
  *   dl[e] = s[e] (ds[e] - sum_f s[f] ds[f])   softmax
  *   dl[e] = s[e] (1 - s[e]) ds[e]             sigmoid
- * in fp32, rounded to the type of the logits once.  The choice itself has no
- * gradient, and the bias none.
+ * in fp32, rounded to the type of the logits once.  With RENORM the ratios
+ * s[e_i] / S are formed from differences of the chosen logits, so that scores
+ * need not be numbers of binary32; S counts as 0 where mx_router's does with
+ * the sigmoid (every chosen logit is below -709.78), and never with the
+ * softmax (there too the gradient is that of the ratios).  The choice itself
+ * has no gradient, and the bias none.
  *   logits    as mx_router; experts int32 [T][k], dweights float32 [T][k]
  *   dscores   NULL, or float32 [T][E]: a gradient of the scores output
  *   dlogits   float32 or bf16, as the logits, [T][ldd] out (E columns

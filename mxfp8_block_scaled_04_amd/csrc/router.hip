@@ -608,7 +608,15 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterBackwar
             if (mine != kLowest) s = exp_below(mine - top);  // (the softmax's sum cancels)
         }
         if (renorm) {
-            const float total = team_sum<W>(s);
+            float total = team_sum<W>(s);
+            if (sigmoid && __ballot(!(total >= 0.5f)) != 0) {
+                // All chosen logits of a token are negative: s over the largest one's e^l, so that no s has to be held; 0
+                // where mx_router's sum is, of binary64 (1 + e^-l is infinite from here on).
+                const float top = team_reduce<W>(mine, larger);
+                const float over_top = top > -709.782715f ? exp_below(mine - top) * rest : mine != mine ? mine : 0.0f;
+                const float sum = team_sum<W>(over_top);
+                if (!(total >= 0.5f)) s = over_top, total = sum;
+            }
             const float p = s == 0.0f ? 0.0f : s / total;
             const float average = team_sum<W>(p == 0.0f ? 0.0f : p * part);
             part = p == 0.0f ? 0.0f : p * (part - average);
