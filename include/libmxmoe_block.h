@@ -56,6 +56,10 @@ enum {
  * Choices are compared in binary64, so that ones that binary32 cannot tell
  * apart are in the order of the formulas (without a bias, and with one choice
  * per group score, the logits themselves are compared: the order is the same).
+ * Weights are formed in binary64 and rounded once, but for the softmax's sum
+ * over all experts, which is of binary32 (weights without RENORM: a few
+ * steps), as the scores output is.  A token's results do not depend on the
+ * others', only on the sizes.
  * A NaN, in a logit or choice, counts as larger than every number, and its
  * weights are NaN.
  * Requires T >= 0, 1 <= E <= 4096, 1 <= k <= 64, 1 <= groups <= 64, E %

@@ -138,6 +138,7 @@ __device__ __forceinline__ void store_values(uint16_t* p, int here, const float 
 // e^x, |x| <= 150 or NaN: the product with log2(e) in two parts, so that the
 // error stays below 3 steps whatever x is.
 __device__ __forceinline__ float exp_of(float x) {
+#pragma clang fp contract(off)  // (a sum of these has the same bits wherever it is formed)
     const float t = x * 1.44269504f;
     float low = __builtin_fmaf(x, 1.44269504f, -t);
     low = __builtin_fmaf(x, 1.92596299e-8f, low);  // log2(e) - fp32(log2(e))
@@ -208,11 +209,12 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
     constexpr int kTeams = kThreads / W;
     constexpr int kList = 2 * W;  // candidates that are ranked
     __shared__ uint64_t list_key[kTeams][kList];
-    __shared__ double list_score[kTeams][kList];
+    __shared__ double list_part[kTeams][kList];
     __shared__ int32_t list_expert[kTeams][kList];
     __shared__ uint64_t chosen_key[kTeams][W + 1];
-    __shared__ double chosen_score[kTeams][W];
+    __shared__ double chosen_part[kTeams][W];
     __shared__ int32_t chosen_expert[kTeams][W];
+    __shared__ float sum32[kTeams];
     const int lane = threadIdx.x & 63;
     const int a = lane & (W - 1);
     const int team = threadIdx.x / W;
@@ -267,20 +269,18 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
             part = team_sum<W>(part);
             sum = (double)part;
             over = part == 0.0f ? 0.0f : 1.0f / part;
+            if (a == 0) sum32[team] = part;
 #pragma unroll
             for (int j = 0; j < ITEMS; ++j) c[j] *= over;
         }
         if (g.scores != nullptr) store_values<ITEMS>(g.scores + token * g.E + base, here, c);
     }
-    // (of finite logits, or NaN)
-    const auto score64 = [&](float v) {
-        return sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / sum;
-    };
-    const auto choice64 = [&](int32_t expert, double* score) {  // as a key; 0: cannot be chosen
+    // (of finite logits, or NaN; a softmax's score is this over the sum)
+    const auto part64 = [&](float v) { return sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top); };
+    const auto choice64 = [&](int32_t expert, double* part) {  // as a key; 0: cannot be chosen
         const float v = load_logit(row + expert), b = g.bias != nullptr ? g.bias[expert] : 0.0f;
-        const double s = score64(v);
-        *score = s;
-        return v == kLowest || b == kLowest ? 0 : key_of(by_logit ? (double)v + 0.0 : s + (double)b);
+        const double s = *part = part64(v);
+        return v == kLowest || b == kLowest ? 0 : key_of(by_logit ? (double)v + 0.0 : (sigmoid ? s : s / sum) + (double)b);
     };
     // The softmax's sum above is of binary32, ITEMS terms in a row, 6 joins and 8 half steps of a term off at most (here:
     // twice that): choices that are no more than that part of the largest score apart are formed again with one of binary64
@@ -360,8 +360,8 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
             for (int j = 0; j < ITEMS; ++j) some |= c[j] >= from ? 1ull << j : 0;
             Keys2 u{0, 0};
             while (some != 0) {
-                double s;
-                u.add(choice64(base + __builtin_ctzll(some), &s));
+                double part;
+                u.add(choice64(base + __builtin_ctzll(some), &part));
                 some &= some - 1;
             }
             for (int d = 1; d < lanes_per_group; d *= 2) {
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
         for (int p = 0; p < passes; ++p) {
             const int at = p * W + a;
             if (at >= held && at < entries)
-                list_key[team][at] = choice64(list_expert[team][at], &list_score[team][at]);
+                list_key[team][at] = choice64(list_expert[team][at], &list_part[team][at]);
             else if (at >= entries)
                 list_key[team][at] = 0;
         }
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
             if (at < entries && rank < g.k) {
                 chosen_key[team][rank] = mine;
                 chosen_expert[team][rank] = mine != 0 ? list_expert[team][at] : -1;
-                chosen_score[team][rank] = list_score[team][at];
+                chosen_part[team][rank] = list_part[team][at];
             }
         }
         wave_sync();
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
         if (a < held) {
             list_key[team][a] = chosen_key[team][a];
             list_expert[team][a] = chosen_expert[team][a];
-            list_score[team][a] = chosen_score[team][a];
+            list_part[team][a] = chosen_part[team][a];
         }
         wave_sync();
     }
@@ -496,10 +496,15 @@ __global__ __launch_bounds__(kThreads, ITEMS <= 16 ? 6 : 1) void router_kernel(R
     // lane i < k has choice i (a team has k lanes at least)
     const bool mine = live && a < g.k;
     const int32_t expert = mine && a < held ? chosen_expert[team][a] : -1;
-    double s = expert >= 0 ? chosen_score[team][a] : 0.0;
+    double s = expert >= 0 ? chosen_part[team][a] : 0.0;
+    if (!sigmoid && expert >= 0 && sum != sum) s = sum;  // (a NaN, or +infinity, makes all scores of the token NaN)
     if (renorm) {
         const double total = team_reduce<W>(s, [](double p, double q) { return p + q; });
         s = expert < 0 || total == 0.0 ? 0.0 : s / total;
+    } else if (!sigmoid && expert >= 0) {
+        // of binary32 in every token: `sum` may be another one here, where a token of the wave, this or another, had choices
+        // close to each other
+        s /= (double)sum32[team];
     }
     if (mine) {
         g.experts[token * g.k + a] = expert;
