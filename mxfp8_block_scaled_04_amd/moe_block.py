@@ -55,6 +55,11 @@ class _Norm:
         self.h = x if residual is None else h
         return self.y
 
+    def check(self):
+        """Before a backward pass: there is a forward pass whose rows it reads."""
+        if self.h is None:
+            raise ValueError("backward needs a forward pass before it")
+
     def backward(self, dy, weight, dh, dy2=None):
         mx_rms_norm_backward(dy, self.h, weight, self.rstd, dy2=dy2, dh_in=dh, dh=self.dh, dweight=self.dweight,
                              workspace=self.workspace)
@@ -103,6 +108,7 @@ class MoEBlock:
     def backward(self, dout, dh, norm_weight, gate):
         """After forward: dout bf16 [T, H] and dh (the stream's gradient, or
         None) -> (dh of x and of the residual, dW1, dW2, dgate [E, H], dnorm)."""
+        self.norm.check()
         mx_combine_dweights(dout, self.routed.layer.y, self.routed.slot_of, dweights=self.dweights)
         mx_router_backward(self.logits, self.experts, self.dweights, dlogits=self.dlogits, **self.weighting)
         mx_grouped_gemm_bf16_wgrad(self.dlogits, self.norm.y, self.all_rows, dw=self.dgate,
@@ -115,7 +121,8 @@ class MoEBlock:
 
 class DenseBlock:
     """T tokens of H columns through one SwiGLU layer of width I in MXFP8.
-    training=False leaves out what only the backward pass reads."""
+    training=False leaves out the column-wise quantization of y, which only the
+    backward pass reads, and refuses that pass."""
 
     def __init__(self, T, H, I, device="cuda", eps=1e-6, stream_dtype=torch.bfloat16, training=True):
         self.T, self.H, self.I, self.training = T, H, I, training
@@ -136,6 +143,9 @@ class DenseBlock:
         return self.layer.forward_experts(), self.norm.h
 
     def backward(self, dout, dh, norm_weight):
-        """After forward with training=True -> (dh of x and of the residual, dW1, dW2, dnorm)."""
+        """After forward -> (dh of x and of the residual, dW1, dW2, dnorm)."""
+        if not self.training:
+            raise ValueError("a block made with training=False has no backward pass")
+        self.norm.check()
         dy, dW1, dW2 = self.layer.backward(dout)
         return self.norm.backward(dy, norm_weight, dh), dW1, dW2, self.norm.dweight

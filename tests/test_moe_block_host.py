@@ -1,0 +1,38 @@
+"""What the blocks around the experts do on the host, without a GPU: calls
+that they refuse.  Their buffers are on the CPU here, and no call reaches a
+kernel."""
+import pytest
+import torch
+
+from mxfp8_block_scaled_04_amd.moe_block import DenseBlock, MoEBlock
+
+T, K, E, H, I = 6, 2, 8, 256, 256
+
+
+def _moe(**kw):
+    return MoEBlock(T, K, E, H, I, device="cpu", **kw)
+
+
+def _dense(**kw):
+    return DenseBlock(T, H, I, device="cpu", **kw)
+
+
+def _rows(dtype=torch.bfloat16):
+    return torch.zeros((T, H), dtype=dtype)
+
+
+NORM, GATE = torch.zeros(H, dtype=torch.bfloat16), torch.zeros((E, H), dtype=torch.bfloat16)
+
+
+def test_a_block_without_training_has_no_backward_pass():
+    block = _dense(training=False)
+    block.norm.h = _rows()  # (as a forward pass leaves it)
+    with pytest.raises(ValueError, match="training=False"):
+        block.backward(_rows(), None, NORM)
+
+
+def test_backward_needs_a_forward_pass():
+    with pytest.raises(ValueError, match="forward"):
+        _dense().backward(_rows(), None, NORM)
+    with pytest.raises(ValueError, match="forward"):
+        _moe().backward(_rows(), None, NORM, GATE)
