@@ -27,7 +27,7 @@ are its own buffers: they hold until its next call.
 import torch
 
 from . import mx_quantize_cols
-from .block import (mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward, mx_rms_norm_backward_workspace_bytes,
+from .block import (_matrix, _one_gpu, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward, mx_rms_norm_backward_workspace_bytes,
                     mx_router, mx_router_backward)
 from .moe_layer import MoELayer, RoutedMoELayer
 from .training import (mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad, mx_grouped_gemm_bf16_wgrad,
@@ -55,10 +55,12 @@ class _Norm:
         self.h = x if residual is None else h
         return self.y
 
-    def check(self):
-        """Before a backward pass: there is a forward pass whose rows it reads."""
+    def check(self, dout):
+        """Before a backward pass: there is a forward pass whose rows it reads, and dout is of its rows."""
         if self.h is None:
             raise ValueError("backward needs a forward pass before it")
+        _matrix(dout, "dout", (torch.bfloat16,), *self.y.shape)
+        _one_gpu(self.y, dout)
 
     def backward(self, dy, weight, dh, dy2=None):
         mx_rms_norm_backward(dy, self.h, weight, self.rstd, dy2=dy2, dh_in=dh, dh=self.dh, dweight=self.dweight,
@@ -92,7 +94,8 @@ class MoEBlock:
                                           dtype=torch.uint8, device=device)
 
     def quantize_weights(self, W1, W2):
-        """After every change of the experts' weights (bf16, as MoELayer takes them)."""
+        """After every change of the experts' weights: bf16 [E, 2I, H] in swiglu_interleave order and [E, H, I]."""
+        _one_gpu(self.norm.y, W1, W2)
         self.routed.layer.quantize_weights(W1, W2)
 
     def forward(self, x, residual, norm_weight, gate, bias=None):
@@ -108,7 +111,7 @@ class MoEBlock:
     def backward(self, dout, dh, norm_weight, gate):
         """After forward: dout bf16 [T, H] and dh (the stream's gradient, or
         None) -> (dh of x and of the residual, dW1, dW2, dgate [E, H], dnorm)."""
-        self.norm.check()
+        self.norm.check(dout)
         mx_combine_dweights(dout, self.routed.layer.y, self.routed.slot_of, dweights=self.dweights)
         mx_router_backward(self.logits, self.experts, self.dweights, dlogits=self.dlogits, **self.weighting)
         mx_grouped_gemm_bf16_wgrad(self.dlogits, self.norm.y, self.all_rows, dw=self.dgate,
@@ -132,6 +135,7 @@ class DenseBlock:
 
     def quantize_weights(self, W1, W2):
         """After every change of the weights: bf16 [1, 2I, H] in swiglu_interleave order and [1, H, I]."""
+        _one_gpu(self.norm.y, W1, W2)
         self.layer.quantize_weights(W1, W2)
 
     def forward(self, x, residual, norm_weight):
@@ -146,6 +150,6 @@ class DenseBlock:
         """After forward -> (dh of x and of the residual, dW1, dW2, dnorm)."""
         if not self.training:
             raise ValueError("a block made with training=False has no backward pass")
-        self.norm.check()
+        self.norm.check(dout)
         dy, dW1, dW2 = self.layer.backward(dout)
         return self.norm.backward(dy, norm_weight, dh), dW1, dW2, self.norm.dweight
