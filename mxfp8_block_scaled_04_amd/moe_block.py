@@ -20,15 +20,17 @@ new stream; the next block adds the two.
     backward  MoELayer.backward, mx_rms_norm_backward
 
 Gradients of the weights are those of one step (MoELayer's in bf16, the gate's
-and the norm's in float32).  Buffers are allocated once; every step runs in the
+and the norm's in float32).  backward returns the gradient of the sum in the
+stream's type, which the block before takes as its dh, and leaves it in dx in
+bf16, which that block takes as its dout.  Buffers are allocated once; every step runs in the
 library's kernels on the current stream and can be captured.  A block's outputs
 are its own buffers: they hold until its next call.
 """
 import torch
 
 from . import mx_quantize_cols
-from .block import (_matrix, _one_gpu, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward, mx_rms_norm_backward_workspace_bytes,
-                    mx_router, mx_router_backward)
+from .block import (_matrix, _one_gpu, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward,
+                    mx_rms_norm_backward_workspace_bytes, mx_router, mx_router_backward)
 from .moe_layer import MoELayer, RoutedMoELayer
 from .training import (mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad, mx_grouped_gemm_bf16_wgrad,
                        mx_grouped_gemm_bf16_wgrad_workspace_bytes)
@@ -44,6 +46,8 @@ class _Norm:
         self.y = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.rstd = torch.empty(T, dtype=torch.float32, device=device)
         self.dh = torch.empty((T, H), dtype=stream_dtype, device=device)
+        # in bf16, as the sub-layer whose output x is takes it
+        self.dx = self.dh if stream_dtype is torch.bfloat16 else torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.dweight = torch.empty(H, dtype=torch.float32, device=device)
         self.workspace = torch.empty(mx_rms_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=device)
 
@@ -63,8 +67,8 @@ class _Norm:
         _one_gpu(self.y, dout)
 
     def backward(self, dy, weight, dh, dy2=None):
-        mx_rms_norm_backward(dy, self.h, weight, self.rstd, dy2=dy2, dh_in=dh, dh=self.dh, dweight=self.dweight,
-                             workspace=self.workspace)
+        mx_rms_norm_backward(dy, self.h, weight, self.rstd, dy2=dy2, dh_in=dh, dh=self.dh,
+                             dx=None if self.dx is self.dh else self.dx, dweight=self.dweight, workspace=self.workspace)
         return self.dh
 
 
@@ -80,6 +84,7 @@ class MoEBlock:
         self.T, self.k, self.E, self.H, self.I = T, k, E, H, I
         self.routed = RoutedMoELayer(T, k, E, H, I, device)
         self.norm = _Norm(T, H, eps, stream_dtype, device)
+        self.dx = self.norm.dx
         self.weighting = {"score": score, "renorm": renorm, "scale": scale}
         self.choice = {"groups": groups, "groups_kept": groups_kept, "group_top": group_top}
         self.all_rows = torch.tensor([0, T], dtype=torch.int32, device=device)
@@ -132,6 +137,7 @@ class DenseBlock:
         self.all_rows = torch.tensor([0, T], dtype=torch.int32, device=device)
         self.layer = MoELayer(self.all_rows, T, H, I, device)
         self.norm = _Norm(T, H, eps, stream_dtype, device)
+        self.dx = self.norm.dx
 
     def quantize_weights(self, W1, W2):
         """After every change of the weights: bf16 [1, 2I, H] in swiglu_interleave order and [1, H, I]."""
