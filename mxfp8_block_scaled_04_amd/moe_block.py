@@ -23,17 +23,25 @@ Gradients of the weights are those of one step (MoELayer's in bf16, the gate's
 and the norm's in float32).  backward returns the gradient of the sum in the
 stream's type, which the block before takes as its dh, and leaves it in dx in
 bf16, which that block takes as its dout.  Buffers are allocated once; every step runs in the
-library's kernels on the current stream and can be captured.  A block's outputs
+library's kernels on the current stream of the block's GPU and can be captured.  A block's outputs
 are its own buffers: they hold until its next call.
 """
+import contextlib
+
 import torch
 
 from . import mx_quantize_cols
-from .block import (_matrix, _one_gpu, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward,
+from .block import (_current_device, _matrix, _one_gpu, mx_combine_dweights, mx_rms_norm, mx_rms_norm_backward,
                     mx_rms_norm_backward_workspace_bytes, mx_router, mx_router_backward)
 from .moe_layer import MoELayer, RoutedMoELayer
 from .training import (mx_grouped_gemm_bf16, mx_grouped_gemm_bf16_dgrad, mx_grouped_gemm_bf16_wgrad,
                        mx_grouped_gemm_bf16_wgrad_workspace_bytes)
+
+
+def _gpu_of(buffer):
+    """The block's GPU as the current one: the calls of moe_layer and the products run on the current GPU's stream."""
+    at = buffer.get_device()  # -1: not on a GPU
+    return contextlib.nullcontext() if at < 0 or at == _current_device() else torch.cuda.device(at)
 
 
 class _Norm:
@@ -101,30 +109,33 @@ class MoEBlock:
     def quantize_weights(self, W1, W2):
         """After every change of the experts' weights: bf16 [E, 2I, H] in swiglu_interleave order and [E, H, I]."""
         _one_gpu(self.norm.y, W1, W2)
-        self.routed.layer.quantize_weights(W1, W2)
+        with _gpu_of(self.norm.y):
+            self.routed.layer.quantize_weights(W1, W2)
 
     def forward(self, x, residual, norm_weight, gate, bias=None):
         """x bf16 [T, H] (or the stream itself, with residual None), gate bf16
         [E, H], bias float32 [E] or None (for the choice only).  Returns (out
         bf16 [T, H], h): the block's output and the new residual stream."""
-        y = self.norm.forward(x, residual, norm_weight)
-        mx_grouped_gemm_bf16(y, gate.unsqueeze(0), self.all_rows, out=self.logits)
-        mx_router(self.logits, self.k, bias=bias, experts=self.experts, weights=self.weights, **self.choice,
-                  **self.weighting)
-        return self.routed.forward(y, self.experts, self.weights), self.norm.h
+        with _gpu_of(self.norm.y):
+            y = self.norm.forward(x, residual, norm_weight)
+            mx_grouped_gemm_bf16(y, gate.unsqueeze(0), self.all_rows, out=self.logits)
+            mx_router(self.logits, self.k, bias=bias, experts=self.experts, weights=self.weights, **self.choice,
+                      **self.weighting)
+            return self.routed.forward(y, self.experts, self.weights), self.norm.h
 
     def backward(self, dout, dh, norm_weight, gate):
         """After forward: dout bf16 [T, H] and dh (the stream's gradient, or
         None) -> (dh of x and of the residual, dW1, dW2, dgate [E, H], dnorm)."""
         self.norm.check(dout)
-        mx_combine_dweights(dout, self.routed.layer.y, self.routed.slot_of, dweights=self.dweights)
-        mx_router_backward(self.logits, self.experts, self.dweights, dlogits=self.dlogits, **self.weighting)
-        mx_grouped_gemm_bf16_wgrad(self.dlogits, self.norm.y, self.all_rows, dw=self.dgate,
-                                   workspace=self.gate_workspace)
-        mx_grouped_gemm_bf16_dgrad(self.dlogits, gate.unsqueeze(0), self.all_rows, dx=self.dy)
-        dy, dW1, dW2 = self.routed.backward(dout)
-        dx = self.norm.backward(dy, norm_weight, dh, self.dy)
-        return dx, dW1, dW2, self.dgate[0], self.norm.dweight
+        with _gpu_of(self.norm.y):
+            mx_combine_dweights(dout, self.routed.layer.y, self.routed.slot_of, dweights=self.dweights)
+            mx_router_backward(self.logits, self.experts, self.dweights, dlogits=self.dlogits, **self.weighting)
+            mx_grouped_gemm_bf16_wgrad(self.dlogits, self.norm.y, self.all_rows, dw=self.dgate,
+                                       workspace=self.gate_workspace)
+            mx_grouped_gemm_bf16_dgrad(self.dlogits, gate.unsqueeze(0), self.all_rows, dx=self.dy)
+            dy, dW1, dW2 = self.routed.backward(dout)
+            dx = self.norm.backward(dy, norm_weight, dh, self.dy)
+            return dx, dW1, dW2, self.dgate[0], self.norm.dweight
 
 
 class DenseBlock:
@@ -142,20 +153,23 @@ class DenseBlock:
     def quantize_weights(self, W1, W2):
         """After every change of the weights: bf16 [1, 2I, H] in swiglu_interleave order and [1, H, I]."""
         _one_gpu(self.norm.y, W1, W2)
-        self.layer.quantize_weights(W1, W2)
+        with _gpu_of(self.norm.y):
+            self.layer.quantize_weights(W1, W2)
 
     def forward(self, x, residual, norm_weight):
         """x bf16 [T, H] (or the stream itself, with residual None).  Returns (out bf16 [T, H], h)."""
-        X = self.layer.x
-        y = self.norm.forward(x, residual, norm_weight, X.q, X.s)
-        if self.training:
-            mx_quantize_cols(y, self.all_rows, X.Mcap, X.qT, X.sT, X.P)
-        return self.layer.forward_experts(), self.norm.h
+        with _gpu_of(self.norm.y):
+            X = self.layer.x
+            y = self.norm.forward(x, residual, norm_weight, X.q, X.s)
+            if self.training:
+                mx_quantize_cols(y, self.all_rows, X.Mcap, X.qT, X.sT, X.P)
+            return self.layer.forward_experts(), self.norm.h
 
     def backward(self, dout, dh, norm_weight):
         """After forward -> (dh of x and of the residual, dW1, dW2, dnorm)."""
         if not self.training:
             raise ValueError("a block made with training=False has no backward pass")
         self.norm.check(dout)
-        dy, dW1, dW2 = self.layer.backward(dout)
-        return self.norm.backward(dy, norm_weight, dh), dW1, dW2, self.norm.dweight
+        with _gpu_of(self.norm.y):
+            dy, dW1, dW2 = self.layer.backward(dout)
+            return self.norm.backward(dy, norm_weight, dh), dW1, dW2, self.norm.dweight
