@@ -126,6 +126,12 @@ def _whole(t, name, dtypes, *shape):
         raise ValueError(f"{name} must be a contiguous tensor of {' x '.join(map(str, shape))}")
 
 
+def _check_int32(bits):
+    """bits: the bitwise or of numbers that the call takes as int32 (ctypes would drop what is above)."""
+    if not -0x80000000 <= bits <= 0x7FFFFFFF:
+        raise ValueError("the numbers of experts, choices and groups must be below 2^31")
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -151,6 +157,9 @@ def mx_router(logits, k, bias=None, groups=1, groups_kept=None, group_top=2, sco
     ldl = _matrix(logits, "logits", (_FP32, _BF16))
     T, E = logits.shape
     flags = _flags(score, renorm, logits)
+    if groups_kept is None:
+        groups_kept = groups
+    _check_int32(E | k | groups | groups_kept | group_top)
     dev = logits.device
     if experts is None:
         experts = _empty(T, k, _INT32, dev, stream)
@@ -167,9 +176,8 @@ def mx_router(logits, k, bias=None, groups=1, groups_kept=None, group_top=2, sco
     if bias is not None:
         _whole(bias, "bias", (_FP32,), E)
     at = _one_gpu(logits, bias, experts, weights, scores)
-    _call("mx_router", at, stream, logits.data_ptr(), ldl, T, E, _at(bias), groups,
-          groups if groups_kept is None else groups_kept, group_top, k, scale, flags, experts.data_ptr(),
-          weights.data_ptr(), _at(scores))
+    _call("mx_router", at, stream, logits.data_ptr(), ldl, T, E, _at(bias), groups, groups_kept, group_top, k,
+          scale, flags, experts.data_ptr(), weights.data_ptr(), _at(scores))
     return experts, weights, scores
 
 
@@ -187,6 +195,7 @@ def mx_router_backward(logits, experts, dweights, dscores=None, score="softmax",
     if dscores is not None:
         _whole(dscores, "dscores", (_FP32,), T, E)
     flags = _flags(score, renorm, logits)
+    _check_int32(E | k)
     ldd = E
     if dlogits is None:
         dlogits = _empty(T, E, logits.dtype, logits.device, stream)
@@ -207,6 +216,7 @@ def mx_combine_dweights(dout, y, slot_of, dweights=None, stream=None):
     ldy = _matrix(y, "y", (_BF16,), y.shape[0], N)
     k = slot_of.shape[1] if slot_of.dim() == 2 else 0
     _whole(slot_of, "slot_of", (_INT32,), T, k)
+    _check_int32(k)
     if dweights is None:
         dweights = _empty(T, k, _FP32, dout.device, stream)
     else:

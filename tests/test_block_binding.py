@@ -96,3 +96,25 @@ def test_dweight_has_a_type_that_the_kernels_write(calls, dtype):
     assert calls == []
     for d in (torch.bfloat16, torch.float32):
         assert B.mx_rms_norm_backward(x, x, w, r, dweight=d)[2].dtype is d
+
+
+def test_numbers_beyond_32_bits_are_refused(calls):
+    """(2^32 + 8 experts would be taken for 8.)"""
+    many, few = torch.empty((1, 2 ** 32 + 8), device="meta"), torch.zeros(1, 8)
+    with pytest.raises(ValueError, match="below 2"):
+        B.mx_router(many, 2)
+    for kw in ({"groups": 2 ** 32 + 1}, {"groups_kept": 2 ** 32 + 1}, {"group_top": 2 ** 32 + 1}, {"groups": 1 - 2 ** 32}):
+        with pytest.raises(ValueError, match="below 2"):
+            B.mx_router(few, 2, **kw)
+    none = torch.zeros((0, 8))
+    with pytest.raises(ValueError, match="below 2"):
+        B.mx_router(none, 2 ** 32 + 2)
+    i = torch.zeros((1, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="below 2"):
+        B.mx_router_backward(many, i, torch.zeros(1, 2))
+    with pytest.raises(ValueError, match="below 2"):
+        B.mx_combine_dweights(torch.zeros((1, 8), dtype=torch.bfloat16), torch.zeros((1, 8), dtype=torch.bfloat16),
+                              torch.empty((1, 2 ** 32 + 2), dtype=torch.int32, device="meta"))
+    assert calls == []
+    B.mx_router(few, 2, groups=4, groups_kept=2)
+    assert [c[0] for c in calls] == ["mx_router"]
