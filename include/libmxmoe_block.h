@@ -53,6 +53,8 @@ enum {
  *   experts  int32 [T][k] out; weights float32 [T][k] out
  *   scores   NULL, or float32 [T][E] out: all scores (of masked experts too;
  *            zeros for a token whose logits are all -infinity)
+ * Outputs overlap nothing else: logits are read again after scores are written
+ * (scores in the place of logits: MX_ERR_SHAPE).
  * Choices are compared in binary64, so that ones that binary32 cannot tell
  * apart are in the order of the formulas (without a bias, and with one choice
  * per group score, the logits themselves are compared: the order is the same).

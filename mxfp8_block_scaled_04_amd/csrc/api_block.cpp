@@ -63,6 +63,7 @@ mx_status mx_router(const void* logits, int64_t ldl, int64_t T, int32_t E, const
     if (!aligned(logits, flags & MX_ROUTER_LOGITS_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(experts, 4) ||
         !aligned(weights, 4) || !aligned(scores, 4))
         return MX_ERR_ALIGN;
+    if ((const void*)scores == logits) return MX_ERR_SHAPE;
     const mx::RouterArgs a{logits, ldl, T, E, bias, groups, groups_kept, group_top, k, scale, flags, experts, weights,
                            scores};
     return from_hip(mx::launch_router(a, (hipStream_t)stream));

@@ -72,6 +72,12 @@ def test_router_refusals():
     assert f(a2=0, a0=None, a11=None, a12=None) == OK
 
 
+def test_router_scores_in_the_place_of_logits_are_refused():
+    """(The router reads logits again after it has written scores.)"""
+    f = _variants(B._lib().mx_router, (FAKE, 64, 5, 64, FAKE, 4, 2, 2, 8, 1.0, 0, FAKE, FAKE, FAKE, None))
+    assert f() == SHAPE
+
+
 def test_router_backward_refusals():
     # (logits, ldl, T, E, experts, dweights, dscores, k, scale, flags, dlogits, ldd, stream)
     f = _variants(B._lib().mx_router_backward, (FAKE, 64, 5, 64, FAKE, FAKE, FAKE, 8, 1.0, 0, FAKE, 64, None))
