@@ -62,8 +62,8 @@ enum {
  * over all experts, which is of binary32 (weights without RENORM: a few
  * steps), as the scores output is.  A token's results do not depend on the
  * others', only on the sizes.
- * A NaN, in a logit or choice, counts as larger than every number, and its
- * weights are NaN.
+ * A NaN, in a logit or choice, counts as larger than every number; that of a
+ * logit makes its weight NaN (with RENORM or the softmax all of the token's).
  * Requires T >= 0, 1 <= E <= 4096, 1 <= k <= 64, 1 <= groups <= 64, E %
  * groups == 0, 1 <= groups_kept <= groups, k <= groups_kept E / groups,
  * group_top 1 or 2, ldl >= E, finite scale (MX_ERR_SHAPE); pointers aligned to

@@ -70,9 +70,15 @@ __device__ __forceinline__ Eight load_kept(const uint16_t* p) { return unpack(*r
 __device__ __forceinline__ Eight load_kept(const float* p) { return load_raw(p, false); }
 
 // Outputs of large calls leave the caches before anything reads them: from
-// 2^25 elements on, where a call's rows pass the 256 MB of the Infinity Cache,
-// their stores are non-temporal (forward 370 -> 353 us, backward 454 -> 415);
-// smaller ones are left where the next kernel finds them.
+// 2^25 elements on their stores are non-temporal (forward 370 -> 353 us, backward
+// 454 -> 415), and so are the loads of bf16; smaller ones are left where the next
+// kernel finds them.  Not the stores of a float32 stream (above).  The number is
+// where calls with a residual and MXFP8 rows pass the 256 MB of the Infinity
+// Cache (9 bytes an element, cached against non-temporal: 16384 and 32768 rows
+// of 1024 26.0 and 29.3 us, 58.3 and 56.8).  Calls of fewer bytes an element
+// pass it later and are slower in between (4 bytes, without a residual: 65536
+// rows 47.9 and 50.4, 131072 101.0 and 93.7; 6 bytes, backward: 32768 rows 44.7
+// and 46.3, 65536 82.0 and 79.2).
 constexpr int64_t kFar = (int64_t)1 << 25;
 __device__ __forceinline__ void store_out(void* p, uint4 d, bool far) {
     if (far) store_stream16(p, d);
@@ -503,9 +509,11 @@ constexpr int64_t kBackwardOne = 64 * kMaxWaves;  // rows of up to so many vecto
 
 // Up to so many rows (of up to 16384 columns) dweight is computed from the rows
 // again, which are in the caches, instead of from parts: one launch for all of
-// it and no workspace (64 rows of 7168 7.6 -> 5.9
-// us and 3 us less on the host; 1531 of 1480 would take 27 against 11).  Where an output
-// replaces an input, it is computed before.
+// it, no workspace, and 3 us less on the host.  Rows read again against parts:
+// 256 rows of 64 columns 5.1 and 5.7 us, of 1480 5.8 and 7.3, of 7168 7.5 and
+// 11.7, of 16384 15.2 and 17.9; 384 rows of 64 5.7 and 5.8, of 16384 20.2 and
+// 19.1; 1024 rows of 1480 14.5 and 10.5.  Where an output replaces an input, it
+// is computed before.
 constexpr int64_t kFewRows = 256;
 bool few_rows(int64_t M, int64_t N) { return M > 0 && M <= kFewRows && N <= 16 * 64 * kMaxWaves; }
 

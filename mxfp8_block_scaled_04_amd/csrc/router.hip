@@ -21,12 +21,16 @@
 // that binary32 cannot tell apart are formed again from the few largest
 // choices of each group in binary64.
 //
-// What bounds it: vector instructions, about 260 per token at 256 experts and
+// What bounds it: vector instructions, about 250 per token at 256 experts and
 // k = 8 (HBM would take 7 us for what follows).  Measured: 32768 tokens to 8 of
-// 256 experts in 8 groups, sigmoid, bias, float32 logits 20 us; 8191 tokens to
-// 6 of 165 in 3 groups, softmax, all scores written, bf16 9.9; 16 tokens 6.4,
-// the chain of reductions.  k rounds of "the largest that is left" in binary64
-// took 59, 18 and 7.6.
+// 256 experts in 8 groups, sigmoid, bias, float32 logits 21 us (the same in bf16);
+// 8191 tokens to 6 of 165 in 3 groups, softmax, all scores written, bf16 10; 16
+// tokens 6.4, the chain of reductions.  k rounds of "the largest that is left" in
+// binary64 took 59, 18 and 7.6.
+//
+// Six waves a vector unit: the bf16 instances of 16 experts a lane spill 4 to 7
+// registers for it (with five, 32768 tokens to 8 of 256 in 8 groups take as
+// long, to 4 of 128 9.9 us instead of 10.5; float32 spills none).
 #include <type_traits>
 
 #include "mx_bf16.h"

@@ -22,9 +22,12 @@ new stream; the next block adds the two.
 Gradients of the weights are those of one step (MoELayer's in bf16, the gate's
 and the norm's in float32).  backward returns the gradient of the sum in the
 stream's type, which the block before takes as its dh, and leaves it in dx in
-bf16, which that block takes as its dout.  Buffers are allocated once; every step runs in the
-library's kernels on the current stream of the block's GPU and can be captured.  A block's outputs
-are its own buffers: they hold until its next call.
+bf16, which that block takes as its dout.  The router's logits are bf16, as the
+product writes them: equal ones go to the lower index.  Without a residual the
+input is the stream itself, which backward reads again: it has to stay as it is
+until then.  Buffers are allocated once; every step runs in the library's
+kernels on the current stream of the block's GPU and can be captured.  A block's
+outputs are its own buffers: they hold until its next call.
 """
 import contextlib
 
